@@ -530,6 +530,142 @@ W4_API w4_status i8_head_argmax(const float* h, int64_t ldh, const int8_t* table
 W4_API w4_status i8_embed_lookup(const int8_t* table, int64_t ldt, const float* scales, const int32_t* tokens,
                                  int64_t ntok, float* out, int64_t ldo, int64_t K, int64_t V, void* stream);
 
+/* ------------------------------------------------------------------ key-value cache */
+
+/* What a decode step needs between its matmuls: the cache of one attention
+ * layer in pages, the entry point that writes new tokens into it, the
+ * attention of each sequence's newest token over it, and the eviction of the
+ * slots that the attention has used least. Activations are fp32, as
+ * everywhere in this library.
+ *
+ * Element types of a cache. W4_KV_I8 stores each (token, head) row of keys or
+ * of values as int8 codes with one fp32 scale, by the rule of the head's
+ * quantiser (i8_quantize_head): s = max|x| / 127 rounded once to fp32 (1 for
+ * a row of zeros), code = rint(x / s) in fp64, clamped to -127..127; it
+ * stands for code * s. The others store x rounded to nearest. */
+typedef enum w4_kv_type { W4_KV_F32 = 0, W4_KV_F16 = 1, W4_KV_BF16 = 2, W4_KV_I8 = 3 } w4_kv_type;
+
+/* One layer's paged cache. All arrays are the caller's device memory.
+ * - k, v: [num_pages] pages of [kv_heads][page_size][head_dim] elements, pages
+ *   page_stride elements apart (page_stride >= kv_heads * page_size *
+ *   head_dim, a multiple of 16 bytes); 16-byte aligned. head_dim is a
+ *   multiple of 16, at most 256; page_size is any number from 1 to 65536.
+ * - k_scales, v_scales: W4_KV_I8 only (NULL otherwise): fp32 [num_pages]
+ *   [kv_heads][page_size], packed, 4-byte aligned.
+ * - page_table: int32, row b (at b * ldp) names the pages of sequence b in
+ *   order: its slot j lies in page page_table[b * ldp + j / page_size], at
+ *   j % page_size. max_pages entries a row; ldp >= max_pages, or 0 for one row
+ *   that all sequences share. max_pages * page_size, the capacity of a
+ *   sequence, is at most 2^30. Entries behind a sequence's last page are not
+ *   read.
+ * - lengths: int32 [seqs], the slots that each sequence holds. Sequences may
+ *   share pages for reading (a common prefix; a prompt of T tokens is
+ *   attended causally by T "sequences" over one row of pages with lengths
+ *   1 .. T); pages written by kv_append or kv_evict belong to one sequence.
+ * A page id outside [0, num_pages) or a length outside [0, capacity] records
+ * W4_ERR_VALUE in the device error word (w4_device_error); the slots concerned
+ * count as empty (not written, not attended). */
+typedef struct kv_cache {
+  void* k;
+  void* v;
+  float* k_scales;
+  float* v_scales;
+  const int32_t* page_table;
+  int32_t* lengths;
+  int64_t page_stride;
+  int64_t num_pages;
+  int64_t ldp;
+  int64_t max_pages;
+  int64_t seqs;
+  int32_t kv_heads;
+  int32_t page_size;
+  int32_t head_dim;
+  int32_t type;
+} kv_cache;
+
+/* New tokens' keys and values into the cache. k, v: fp32, `tokens` rows of
+ * [kv_heads][head_dim], ldk / ldv elements apart (columns of a qkv matmul's
+ * rows, say), 4-byte aligned.
+ * - cu_tokens: int32 [seqs + 1] on the device, ascending: rows cu_tokens[b] ..
+ *   cu_tokens[b + 1] - 1 go to sequence b, the first to slot lengths[b].
+ *   Rows outside every sequence are not read. NULL: one row for each
+ *   sequence (tokens == seqs).
+ * - lengths_out: int32 [seqs], lengths[b] + the rows given (the capacity at
+ *   most). It may be the cache's own lengths (they advance in place) or
+ *   memory apart from them. Rows beyond the capacity are not written and
+ *   record W4_ERR_VALUE.
+ * A row of W4_KV_I8 that holds an Inf or NaN reads back as NaN. */
+W4_API w4_status kv_append(const kv_cache* c, const float* k, int64_t ldk, const float* v, int64_t ldv,
+                           const int32_t* cu_tokens, int64_t tokens, int32_t* lengths_out, void* stream);
+
+/* Attention of one token per sequence over its cache: for each sequence b and
+ * query head i (key-value head i / (q_heads / kv_heads)),
+ *   s_j = scale * q[b, i] . k_j   for the attended slots j,
+ *   out[b, i] = sum_j softmax(s)_j v_j,  lse[b, i] = log sum_j exp(s_j),
+ * over the slots j < lengths[b], the last `window` of them when window > 0.
+ * A sequence without slots gives out = 0 and lse = -Inf.
+ * - q, out: fp32, seqs rows of [q_heads][head_dim], ldq / ldo elements apart
+ *   (ldo >= q_heads * head_dim); q_heads is a multiple of kv_heads. lse: fp32
+ *   [seqs][q_heads], or NULL. All 4-byte aligned; out and lse overlap nothing
+ *   else.
+ * - acc: NULL, or fp32 with a row of `capacity` weights for each sequence, at
+ *   b * ldacc (ldacc >= capacity): acc[b, j] += sum over the query heads of
+ *   softmax(s)_j, what kv_evict goes by.
+ * - workspace: kv_attend_workspace_size() bytes of device memory, 16-byte
+ *   aligned; needs no zeroing and holds nothing between calls. Calls that may
+ *   run at the same time must not share it.
+ * Sums and the softmax are fp32; K and V enter with their stored values. A
+ * NaN or Inf in q or in an attended slot makes the rows that it reaches
+ * non-finite; what lies in other slots has no effect. Results do not depend
+ * on timing: the same call gives the same bits. */
+W4_API size_t kv_attend_workspace_size(const kv_cache* c, int64_t q_heads, int32_t with_acc);
+W4_API w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, int64_t q_heads, float scale,
+                           int64_t window, float* out, int64_t ldo, float* lse, float* acc, int64_t ldacc,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Cuts each sequence to at most `keep` slots: the last min(recent, keep) of
+ * them, and of the rest those with the largest acc[b, j] (ties to the lower
+ * slot; NaN ranks below everything). The kept slots move to the front, in
+ * their order. A sequence of at most `keep` slots keeps all of them.
+ * - src: the cache; acc: fp32 rows as kv_attend gathers them.
+ * - dst: where the kept slots go: the same descriptor's arrays (in place: k,
+ *   v, scales, page_table and lengths all equal), or a cache of the same
+ *   heads, page_size, head_dim and type, and seqs, whose pages and arrays
+ *   share no memory with src's. Its lengths are set to the kept counts. Kept
+ *   slots beyond dst's capacity are not moved and record W4_ERR_VALUE (the
+ *   length is cut to the capacity).
+ * - acc_out: fp32 rows like acc (acc itself, or apart from it): the kept
+ *   slots' weights move along, and 0 is written behind them up to the old
+ *   length.
+ * - kept: NULL, or int32 rows of `keep` entries ldkept apart: the kept slots'
+ *   old places, -1 behind the last.
+ * - workspace: kv_evict_workspace_size() bytes, 16-byte aligned, no zeroing,
+ *   not shared by calls that may run at the same time. */
+W4_API size_t kv_evict_workspace_size(const kv_cache* src, int64_t keep);
+W4_API w4_status kv_evict(const kv_cache* src, const float* acc, int64_t ldacc, int64_t keep, int64_t recent,
+                          const kv_cache* dst, float* acc_out, int64_t ldacc_out, int32_t* kept, int64_t ldkept,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ scoring */
+
+/* What a row of logits says of a token: for each of M rows of V logits (ldl
+ * apart; as the head entry points write them),
+ *   logp[m] = logits[m, tokens[m]] - lse_m,  lse_m = log sum_v exp(logits[m, v]),
+ *   entropy[m] = -sum_v p_v log p_v,  p_v = exp(logits[m, v] - lse_m),
+ * and the `top` most likely tokens, best first (ties to the lower id, -0 equal
+ * to +0, NaN below everything): top_logp / top_ids [M][top].
+ * - tokens: int32 [M] on the device, or NULL (then logp must be NULL). -1
+ *   scores nothing (logp 0); another id outside [0, V) gives NaN and records
+ *   W4_ERR_VALUE in the device error word.
+ * - logp, entropy, top_logp, top_ids: each may be NULL. 0 <= top <= 32, top <= V.
+ * A logit of -Inf is a token that cannot occur: it adds nothing to the sums.
+ * A row of which every logit is -Inf, or one with a NaN or +Inf, has NaN logp,
+ * entropy and top_logp. One pass over the logits, no workspace. */
+#define W4_TOP_MAX 32
+W4_API w4_status token_logprobs(const float* logits, int64_t ldl, const int32_t* tokens, int64_t M, int64_t V,
+                                int32_t top, float* logp, float* entropy, float* top_logp, int32_t* top_ids,
+                                void* stream);
+
 /* ------------------------------------------------------------------ quantisers */
 
 /* Scale storage of w4_quantize: fp32 (the shipped format, the one every

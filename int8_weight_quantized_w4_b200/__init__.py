@@ -17,6 +17,11 @@ Operations (see include/w4.h for layouts and error behaviour):
   w4i_matmul(x, wt, K, N)                   M = 1 on the tile layout: integer tensor-core MMAs
   i8t_head_repack(table, scales, K, V)      the head in the tensor cores' tile layout (once, at load)
   i8t_head_logits(h, tiles, K, V) / _argmax M <= 8 rows on the tensor-core head
+  KvCache(k, v, page_table, lengths)        one layer's paged key-value cache
+  kv_append(cache, k, v)                    new tokens' keys and values into it
+  kv_attend(q, cache)                       attention of each sequence's newest token over it
+  kv_evict(cache, acc, keep)                the slots that the attention has used least leave it
+  token_logprobs(logits, tokens, top)       log probabilities, entropy, alternatives from logits
   w4_quantize(w, block, scale_type)         the dq4 quantiser (GPU)
   i8_quantize_head(w)                       the embedding_int8 quantiser (GPU)
   pack_nibbles / unpack_nibbles             host-side UINT4 packing
@@ -30,7 +35,8 @@ from typing import Sequence
 import numpy as np
 
 from . import _lib
-from ._lib import ACTS, GROUP_MAX, PATHS, STATUS, W4Desc, W4LibraryMissing, W4RDesc  # noqa: F401
+from ._lib import (ACTS, GROUP_MAX, KV_TYPES, PATHS, STATUS, TOP_MAX, KvCacheDesc, W4Desc,  # noqa: F401
+                   W4LibraryMissing, W4RDesc)
 
 
 class W4Error(RuntimeError):
@@ -536,6 +542,232 @@ def i8_embed_lookup(table, scales, tokens, K: int, V: int, ldt: int | None = Non
                                _stream_handle(stream))
     _check(st, "i8_embed_lookup")
     return out
+
+
+# ---------------------------------------------------------------- key-value cache
+
+class KvCache:
+    """One layer's paged key-value cache: the caller's tensors, checked once.
+
+    k, v: [pages, kv_heads, page_size, head_dim] of float32, float16, bfloat16
+    or int8 (k_scales / v_scales: fp32 [pages, kv_heads, page_size]); a page is
+    contiguous, pages may lie further apart (a slice of all layers' pages).
+    page_table: int32 [seqs, max_pages], rows of page ids (`expand` of one row
+    shares it); lengths: int32 [seqs], the slots held. All on one CUDA device.
+    """
+
+    def __init__(self, k, v, page_table, lengths, k_scales=None, v_scales=None):
+        torch = _torch()
+        kind = KV_TYPES.get(str(k.dtype).replace("torch.", ""))
+        if kind is None or v.dtype != k.dtype:
+            raise ValueError(f"k and v must both be one of {sorted(KV_TYPES)}")
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must be [pages, kv_heads, page_size, head_dim], of one shape")
+        P, H, S, D = k.shape
+        for name, t in (("k", k), ("v", v)):
+            if P > 0 and t[0].numel() > 0 and not t[0].is_contiguous():
+                raise ValueError(f"a page of {name} must be contiguous")
+        if P > 1 and k.stride(0) != v.stride(0):
+            raise ValueError("the pages of k and v must lie equally far apart")
+        if (kind == KV_TYPES["int8"]) != (k_scales is not None and v_scales is not None) or \
+                (k_scales is None) != (v_scales is None):
+            raise ValueError("an int8 cache needs k_scales and v_scales, another has none")
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (P, H, S) or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous fp32 [pages, kv_heads, page_size]")
+        if page_table.dtype != torch.int32 or page_table.dim() != 2:
+            raise ValueError("page_table must be int32 [seqs, max_pages]")
+        B, MP = page_table.shape
+        if MP > 1 and page_table.stride(1) != 1:
+            raise ValueError("the rows of page_table must be contiguous")
+        if lengths.dtype != torch.int32 or tuple(lengths.shape) != (B,) or not lengths.is_contiguous():
+            raise ValueError("lengths must be a contiguous int32 [seqs]")
+        for t in (v, page_table, lengths, k_scales, v_scales):
+            if t is not None and t.device != k.device:
+                raise ValueError("all tensors of a cache must be on one device")
+        if not k.is_cuda:
+            raise ValueError("a cache lies in device memory: its tensors must be CUDA tensors")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.page_table, self.lengths = page_table, lengths
+        self.device, self.seqs, self.kv_heads, self.page_size, self.head_dim = k.device, B, H, S, D
+        self.capacity = MP * S
+        self.desc = KvCacheDesc(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(lengths),
+                                k.stride(0) if P > 1 else H * S * D, P, page_table.stride(0) if B > 1 else MP, MP, B,
+                                H, S, D, kind)
+        self._ref = C.byref(self.desc)
+        self._need = {}  # (operation, sizes) -> workspace bytes
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, page_size: int, head_dim: int, page_table, dtype):
+        """A cache of fresh pages; every sequence of page_table is empty."""
+        torch = _torch()
+        shape, dev = (pages, kv_heads, page_size, head_dim), page_table.device
+        scales = [torch.zeros(shape[:3], device=dev) for _ in range(2)] if dtype == torch.int8 else [None, None]
+        return cls(torch.zeros(shape, dtype=dtype, device=dev), torch.zeros(shape, dtype=dtype, device=dev), page_table,
+                   torch.zeros(page_table.shape[0], dtype=torch.int32, device=dev), *scales)
+
+
+def _rows3(t, name: str, rows: int | None, heads: int | None, dim: int, device) -> int:
+    """Row stride of an fp32 [rows, heads, dim] tensor whose rows are contiguous."""
+    if t.dim() != 3 or t.dtype is not _torch().float32 or t.device != device:
+        raise ValueError(f"{name} must be an fp32 [rows, heads, head_dim] tensor on {device}")
+    n, h, d = t.shape
+    if (rows is not None and n != rows) or (heads is not None and h != heads) or d != dim:
+        raise ValueError(f"{name} is {tuple(t.shape)}, expected [{rows}, {heads}, {dim}]")
+    s = t.stride()
+    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+        raise ValueError(f"a row of {name} must be contiguous")
+    return s[0] if n > 1 else h * d
+
+
+def _vector(t, name: str, dtype, n: int, device) -> int:
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} [{n}] tensor on {device}")
+    return t.data_ptr()
+
+
+def _matrix(t, name: str, dtype, n: int, width: int, device) -> int:
+    """Row stride of an [n, >= width] tensor with contiguous rows."""
+    if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != n or t.shape[1] < width or t.device != device or \
+            (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a {dtype} [{n}, {width}] tensor with contiguous rows on {device}")
+    return t.stride(0) if n > 1 else max(width, 1)
+
+
+class _On:
+    """Makes a tensor's device current, and `stream` if one is given: what is
+    allocated inside belongs to the stream that the call runs on."""
+
+    def __init__(self, device, stream):
+        self.cuda = _torch().cuda
+        self.index, self.was = device.index, self.cuda.current_device()
+        self.stream = None if stream is None else self.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.index != self.was:
+            self.cuda.set_device(self.index)
+        if self.stream is not None:
+            self.stream.__enter__()
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        if self.index != self.was:
+            self.cuda.set_device(self.was)
+
+
+def kv_append(cache: KvCache, k, v, cu_tokens=None, lengths_out=None, stream=None):
+    """New tokens' keys and values (fp32 [tokens, kv_heads, head_dim], columns
+    of qkv rows for instance) to the ends of their sequences: rows
+    cu_tokens[b] .. cu_tokens[b + 1] - 1 (int32 [seqs + 1]) to sequence b, or
+    one row each without cu_tokens. The lengths advance in place, or go to
+    lengths_out (int32 [seqs]); returns them."""
+    torch = _torch()
+    dev = cache.device
+    n = k.shape[0]
+    ldk = _rows3(k, "k", None, cache.kv_heads, cache.head_dim, dev)
+    ldv = _rows3(v, "v", n, cache.kv_heads, cache.head_dim, dev)
+    cu = 0 if cu_tokens is None else _vector(cu_tokens, "cu_tokens", torch.int32, cache.seqs + 1, dev)
+    if lengths_out is None:
+        lengths_out = cache.lengths
+    out = _vector(lengths_out, "lengths_out", torch.int32, cache.seqs, dev)
+    with _On(dev, stream):
+        _check(lib().kv_append(cache._ref, k.data_ptr(), ldk, v.data_ptr(), ldv, cu, n, out, _stream_handle(stream)),
+               "kv_append")
+    return lengths_out
+
+
+def kv_attend(q, cache: KvCache, scale: float | None = None, window: int = 0, out=None, lse=None, acc=None, ws=None,
+              stream=None):
+    """out [seqs, q_heads, head_dim]: attention of the queries q (fp32, one
+    token per sequence, row stride free) over each sequence's slots, the last
+    `window` of them when it is positive; scale defaults to head_dim ** -0.5.
+    lse: fp32 [seqs, q_heads], filled. acc: fp32 [seqs, >= capacity], each
+    slot's weight summed over the query heads is added."""
+    torch = _torch()
+    dev, B, D = cache.device, cache.seqs, cache.head_dim
+    ldq = _rows3(q, "q", B, None, D, dev)
+    Hq = q.shape[1]
+    ldo = Hq * D if out is None else _rows3(out, "out", B, Hq, D, dev)
+    if lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != (B, Hq) or
+                            not lse.is_contiguous() or lse.device != dev):
+        raise ValueError(f"lse must be a contiguous fp32 [{B}, {Hq}] tensor on {dev}")
+    ldacc = 0 if acc is None else _matrix(acc, "acc", torch.float32, B, cache.capacity, dev)
+    with _On(dev, stream):
+        key = (Hq, acc is not None)
+        need = cache._need.get(key)
+        if need is None:
+            need = cache._need[key] = int(lib().kv_attend_workspace_size(cache._ref, Hq, int(acc is not None)))
+        if out is None:
+            out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+        # torch hands the workspace out again only behind this call on its
+        # stream, and a captured call's belongs to its graph
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(lib().kv_attend(cache._ref, q.data_ptr(), ldq, Hq, D ** -0.5 if scale is None else scale, window,
+                               out.data_ptr(), ldo, _ptr(lse), _ptr(acc), ldacc, _ptr(ws),
+                               0 if ws is None else ws.numel() * ws.element_size(), _stream_handle(stream)),
+               "kv_attend")
+    return out
+
+
+def kv_evict(cache: KvCache, acc, keep: int, recent: int = 0, dst: KvCache | None = None, acc_out=None, kept=None,
+             ws=None, stream=None):
+    """Cuts every sequence to `keep` slots: its last `recent` ones and those
+    with the largest acc (fp32 [seqs, >= capacity], as kv_attend gathers it;
+    ties to the lower slot). The kept slots move to the front in their order,
+    in place or into dst (a cache of other pages); acc moves along, in place
+    or into acc_out. kept: int32 [seqs, >= keep], filled with the kept slots'
+    old places and -1. Returns the new lengths."""
+    torch = _torch()
+    dev, B = cache.device, cache.seqs
+    if dst is None:
+        dst = cache
+    elif dst.device != dev:
+        raise ValueError("dst must be on the cache's device")
+    if acc_out is None:
+        acc_out = acc
+    ld = _matrix(acc, "acc", torch.float32, B, cache.capacity, dev)
+    ldo = _matrix(acc_out, "acc_out", torch.float32, B, cache.capacity, dev)
+    ldk = 0 if kept is None else _matrix(kept, "kept", torch.int32, B, keep, dev)
+    with _On(dev, stream):
+        need = int(lib().kv_evict_workspace_size(cache._ref, keep))
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(lib().kv_evict(cache._ref, acc.data_ptr(), ld, keep, recent, dst._ref, acc_out.data_ptr(), ldo,
+                              _ptr(kept), ldk, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                              _stream_handle(stream)), "kv_evict")
+    return dst.lengths
+
+
+# ---------------------------------------------------------------- scoring
+
+def token_logprobs(logits, tokens=None, top: int = 0, stream=None):
+    """Per row of logits (fp32 [M, V], as the head writes them): (logp [M] of
+    tokens (int32 [M], -1 scores nothing), entropy [M], the `top` best tokens'
+    top_logp [M, top] and top_ids int32 [M, top], best first). logp is None
+    without tokens, the last two without top."""
+    torch = _torch()
+    if logits.dim() == 1:
+        logits = logits.view(1, -1)
+    M, V = logits.shape
+    dev = logits.device
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    ld = _matrix(logits, "logits", torch.float32, M, V, dev)
+    t = 0 if tokens is None else _vector(tokens, "tokens", torch.int32, M, dev)
+    logp = top_logp = top_ids = None
+    f32 = {"dtype": torch.float32, "device": dev}
+    with _On(dev, stream):
+        if tokens is not None:
+            logp = torch.empty(M, **f32)
+        entropy = torch.empty(M, **f32)
+        if top > 0:
+            top_logp = torch.empty((M, top), **f32)
+            top_ids = torch.empty((M, top), dtype=torch.int32, device=dev)
+        _check(lib().token_logprobs(logits.data_ptr(), ld, t, M, V, top, _ptr(logp), entropy.data_ptr(),
+                                    _ptr(top_logp), _ptr(top_ids), _stream_handle(stream)), "token_logprobs")
+    return logp, entropy, top_logp, top_ids
 
 
 # ---------------------------------------------------------------- quantisers

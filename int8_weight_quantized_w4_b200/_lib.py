@@ -27,6 +27,8 @@ W4_OK, W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN, W4_ERR_DEVICE, W4_ERR_CUDA, W4_E
     W4_ERR_VALUE = range(9)
 PATHS = {"auto": 0, "gemv": 1, "generic": 2, "tc": 3}
 ACTS = {"none": 0, "gelu_tanh": 1, "gelu_erf": 2}
+KV_TYPES = {"float32": 0, "float16": 1, "bfloat16": 2, "int8": 3}
+TOP_MAX = 32
 ABI_VERSION = 6
 GROUP_MAX = 48
 
@@ -67,6 +69,27 @@ class W4RDesc(C.Structure):
         ("ldr", C.c_int64),
         ("act", C.c_int32),
         ("reserved", C.c_int32),
+    ]
+
+
+class KvCacheDesc(C.Structure):
+    """kv_cache: one layer's paged key-value cache."""
+    _fields_ = [
+        ("k", C.c_void_p),
+        ("v", C.c_void_p),
+        ("k_scales", C.c_void_p),
+        ("v_scales", C.c_void_p),
+        ("page_table", C.c_void_p),
+        ("lengths", C.c_void_p),
+        ("page_stride", C.c_int64),
+        ("num_pages", C.c_int64),
+        ("ldp", C.c_int64),
+        ("max_pages", C.c_int64),
+        ("seqs", C.c_int64),
+        ("kv_heads", C.c_int32),
+        ("page_size", C.c_int32),
+        ("head_dim", C.c_int32),
+        ("type", C.c_int32),
     ]
 
 
@@ -128,6 +151,18 @@ SIGNATURES = {
     "i8_head_logits_path": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p,
                                       C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_size_t, C.c_int,
                                       C.c_void_p]),
+    "kv_append": (C.c_int, [C.POINTER(KvCacheDesc), C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p,
+                            C.c_int64, C.c_void_p, C.c_void_p]),
+    "kv_attend_workspace_size": (C.c_size_t, [C.POINTER(KvCacheDesc), C.c_int64, C.c_int32]),
+    "kv_attend": (C.c_int, [C.POINTER(KvCacheDesc), C.c_void_p, C.c_int64, C.c_int64, C.c_float, C.c_int64,
+                            C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_size_t,
+                            C.c_void_p]),
+    "kv_evict_workspace_size": (C.c_size_t, [C.POINTER(KvCacheDesc), C.c_int64]),
+    "kv_evict": (C.c_int, [C.POINTER(KvCacheDesc), C.c_void_p, C.c_int64, C.c_int64, C.c_int64,
+                           C.POINTER(KvCacheDesc), C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p,
+                           C.c_size_t, C.c_void_p]),
+    "token_logprobs": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int32, C.c_void_p,
+                                 C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
     "w4_quantize": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_int32, C.c_int32, C.c_void_p,
                               C.c_void_p, C.c_void_p, C.c_void_p]),
     "i8_quantize_head": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p,

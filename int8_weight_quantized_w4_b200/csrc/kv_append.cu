@@ -1,0 +1,289 @@
+// kv_append: new tokens' keys and values into the pages of a cache, and the
+// descriptor checks that the cache's entry points share.
+//
+// Bound by its bytes (fp32 rows in, stored rows out) for prompts and by
+// latency for a decode step. A token is one CTA, so that its place in the
+// cache (a search in cu_tokens, the length, the page: three dependent reads)
+// is found once; its 2 x heads rows of head_dim go to half-warps, 16 lanes of
+// 4 elements wide, which is what a row's maximum (int8) is reduced over.
+#include "kv_cache.cuh"
+
+namespace w4host {
+
+w4_status check_cache(const kv_cache* c, const char* what, w4kv::View* out) {
+  if (c == nullptr) return fail(W4_ERR_NULL, "%s is NULL", what);
+  if (c->type < W4_KV_F32 || c->type > W4_KV_I8) return fail(W4_ERR_VALUE, "%s: unknown element type %d", what, int(c->type));
+  if (c->seqs < 0 || c->num_pages < 0 || c->max_pages < 0) return fail(W4_ERR_SHAPE, "%s: negative size", what);
+  if (c->kv_heads < 1 || c->kv_heads > 4096) return fail(W4_ERR_SHAPE, "%s: kv_heads=%d is outside 1..4096", what, int(c->kv_heads));
+  if (c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16 != 0)
+    return fail(W4_ERR_SHAPE, "%s: head_dim=%d is not a multiple of 16 up to 256", what, int(c->head_dim));
+  if (c->page_size < 1 || c->page_size > 65536) return fail(W4_ERR_SHAPE, "%s: page_size=%d is outside 1..65536", what, int(c->page_size));
+  if (c->num_pages > 0x7fffffff || c->seqs > 65535)
+    return fail(W4_ERR_SHAPE, "%s: num_pages must be below 2^31 and seqs at most 65535", what);
+  if (c->max_pages > (int64_t(1) << 30) / c->page_size)
+    return fail(W4_ERR_SHAPE, "%s: max_pages * page_size is above 2^30", what);
+  const int64_t es = w4kv::elem_bytes(c->type);
+  const int64_t page = int64_t(c->kv_heads) * c->page_size * c->head_dim;
+  if (c->page_stride < page || c->page_stride > (int64_t(1) << 40) || c->page_stride * es % 16 != 0)
+    return fail(W4_ERR_SHAPE, "%s: page_stride=%lld is below a page's %lld elements or no multiple of 16 bytes", what,
+                (long long)c->page_stride, (long long)page);
+  if (c->ldp != 0 && c->ldp < c->max_pages) return fail(W4_ERR_SHAPE, "%s: ldp=%lld < max_pages", what, (long long)c->ldp);
+  if (c->seqs > 0) {
+    if (c->lengths == nullptr) return fail(W4_ERR_NULL, "%s: lengths is NULL", what);
+    if (c->max_pages > 0 && (c->page_table == nullptr || c->k == nullptr || c->v == nullptr))
+      return fail(W4_ERR_NULL, "%s: k, v and page_table must not be NULL", what);
+    if (c->type == W4_KV_I8 && c->max_pages > 0 && (c->k_scales == nullptr || c->v_scales == nullptr))
+      return fail(W4_ERR_NULL, "%s: an int8 cache needs k_scales and v_scales", what);
+  }
+  if (c->type != W4_KV_I8 && (c->k_scales != nullptr || c->v_scales != nullptr))
+    return fail(W4_ERR_VALUE, "%s: scales belong to an int8 cache only", what);
+  const auto bits = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+  if ((bits(c->k) | bits(c->v)) & 15) return fail(W4_ERR_ALIGN, "%s: k and v must be 16-byte aligned", what);
+  if ((bits(c->k_scales) | bits(c->v_scales) | bits(c->page_table) | bits(c->lengths)) & 3)
+    return fail(W4_ERR_ALIGN, "%s: scales, page_table and lengths must be 4-byte aligned", what);
+  out->k = c->k;
+  out->v = c->v;
+  out->ks = c->k_scales;
+  out->vs = c->v_scales;
+  out->table = c->page_table;
+  out->lengths = c->lengths;
+  out->page_stride = c->page_stride;
+  out->ldp = c->ldp;
+  out->num_pages = static_cast<int32_t>(c->num_pages);
+  out->seqs = static_cast<int32_t>(c->seqs);
+  out->heads = c->kv_heads;
+  out->slots_per_page = c->page_size;
+  out->dim = c->head_dim;
+  out->capacity = static_cast<int32_t>(c->max_pages * c->page_size);
+  return W4_OK;
+}
+
+}  // namespace w4host
+
+namespace {
+
+using namespace w4kv;
+
+constexpr int kThreads = 256;
+constexpr int kRowLanes = 16;
+constexpr int kRowVecs = 4;  // of 4 elements: 16 lanes x 4 x 4 = 256, the largest head_dim
+
+struct AppendParams {
+  View c;
+  const float* k;
+  const float* v;
+  int64_t ldk, ldv;
+  const int32_t* cu;
+  int64_t tokens;
+  int32_t* lengths_out;  // NULL: written by advance_kernel
+  int32_t vec;           // both inputs' rows are 16-byte aligned
+  ErrorWord* err;
+};
+
+// Rows of sequence b, by cu_tokens (one each without it).
+__device__ __forceinline__ int32_t rows_of(const AppendParams& p, int32_t b) {
+  if (p.cu == nullptr) return 1;
+  const int64_t n = int64_t(p.cu[b + 1]) - p.cu[b];
+  if (n < 0) w4dev::record_error(p.err, W4_ERR_VALUE, w4dev::K_KV_APPEND, b);
+  return n < 0 ? 0 : static_cast<int32_t>(n > 0x3fffffff ? 0x3fffffff : n);
+}
+
+__device__ __forceinline__ int32_t advanced(const AppendParams& p, int32_t b) {
+  const int32_t n = held_length(p.c, b, p.err, w4dev::K_KV_APPEND) + rows_of(p, b);
+  return n > p.c.capacity ? p.c.capacity : n;
+}
+
+// The sequence whose rows hold row t: how many of cu[1..seqs] are <= t, by
+// whole-warp steps that cut the range 32-fold.
+__device__ int32_t sequence_of(const AppendParams& p, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  int32_t lo = 0, n = p.c.seqs;  // the answer lies in [lo, lo + n]
+  while (n > 0) {
+    const int32_t step = (n + 31) / 32;
+    const int32_t at = lo + (lane + 1) * step;  // counts entries 1..at
+    const bool below = (lane + 1) * step <= n && p.cu[at] <= t;
+    const int32_t hit = __popc(__ballot_sync(0xffffffffu, below));
+    const int32_t skip = hit * step;
+    n = min(n - skip, step - 1);
+    lo += skip;
+  }
+  return lo;
+}
+
+template <int TYPE>
+__device__ __forceinline__ void store4(void* dst, int64_t at, float4 x, double s) {
+  if constexpr (TYPE == W4_KV_F32) {
+    reinterpret_cast<float4*>(dst)[at / 4] = x;
+  } else if constexpr (TYPE == W4_KV_F16) {
+    const __half2 a = __floats2half2_rn(x.x, x.y), b = __floats2half2_rn(x.z, x.w);
+    uint2 w;
+    w.x = *reinterpret_cast<const uint32_t*>(&a);
+    w.y = *reinterpret_cast<const uint32_t*>(&b);
+    reinterpret_cast<uint2*>(dst)[at / 4] = w;
+  } else if constexpr (TYPE == W4_KV_BF16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+    uint2 w;
+    w.x = *reinterpret_cast<const uint32_t*>(&a);
+    w.y = *reinterpret_cast<const uint32_t*>(&b);
+    reinterpret_cast<uint2*>(dst)[at / 4] = w;
+  } else {
+    // the quotient in fp64, as the definition has it: an fp32 quotient rounds
+    // some values onto a half and then to another code
+    const auto code = [s](float f) {
+      const double q = rint(static_cast<double>(f) / s);
+      return static_cast<uint32_t>(static_cast<int>(fmin(fmax(q, -127.0), 127.0))) & 0xFFu;
+    };
+    reinterpret_cast<uint32_t*>(dst)[at / 4] = code(x.x) | code(x.y) << 8 | code(x.z) << 16 | code(x.w) << 24;
+  }
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const View& c = p.c;
+  // the new lengths, where they go to memory of their own
+  const int64_t b_of_thread = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (p.lengths_out != nullptr && p.cu != nullptr && b_of_thread < c.seqs)
+    p.lengths_out[b_of_thread] = advanced(p, static_cast<int32_t>(b_of_thread));
+  const int64_t t = blockIdx.x;
+  if (t >= p.tokens) return;
+  int32_t b = static_cast<int32_t>(t), slot;
+  if (p.cu == nullptr) {
+    slot = held_length(c, b, p.err, w4dev::K_KV_APPEND);
+    if (p.lengths_out != nullptr) {  // this CTA alone reads lengths[b], so it may be advanced in place
+      __syncthreads();
+      if (threadIdx.x == 0) p.lengths_out[b] = min(slot + 1, c.capacity);
+    }
+  } else {
+    b = sequence_of(p, t);
+    if (b >= c.seqs || p.cu[b] > t || p.cu[b + 1] <= t) return;  // a row of no sequence
+    const int64_t at = held_length(c, b, p.err, w4dev::K_KV_APPEND) + (t - p.cu[b]);
+    slot = static_cast<int32_t>(at < c.capacity ? at : c.capacity);
+  }
+  if (slot >= c.capacity) {
+    if (threadIdx.x == 0) w4dev::record_error(p.err, W4_ERR_VALUE, w4dev::K_KV_APPEND, b);
+    return;
+  }
+  const int32_t page = page_of(c, b, slot / c.slots_per_page, p.err, w4dev::K_KV_APPEND);
+  if (page < 0) return;
+  const int32_t inner = slot % c.slots_per_page;
+  const int lane = threadIdx.x % kRowLanes;
+  const int vecs = c.dim / 4;
+  for (int32_t r0 = 0; r0 < 2 * c.heads; r0 += kThreads / kRowLanes) {
+    const int32_t r = r0 + threadIdx.x / kRowLanes;
+    const bool live = r < 2 * c.heads;
+    const bool is_v = r >= c.heads;
+    const int32_t h = is_v ? r - c.heads : r;
+    const float* src = (is_v ? p.v + t * p.ldv : p.k + t * p.ldk) + int64_t(live ? h : 0) * c.dim;
+    float4 x[kRowVecs];
+    float top = 0.f, poison = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRowVecs; ++i) {
+      const int at = lane + i * kRowLanes;
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (live && at < vecs) {
+        if (p.vec) {
+          x[i] = *reinterpret_cast<const float4*>(src + 4 * at);
+        } else {
+          x[i] = make_float4(src[4 * at], src[4 * at + 1], src[4 * at + 2], src[4 * at + 3]);
+        }
+      }
+      if constexpr (TYPE == W4_KV_I8) {
+        top = fmaxf(fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y))), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
+        poison += x[i].x * 0.f + x[i].y * 0.f + (x[i].z * 0.f + x[i].w * 0.f);  // NaN for an Inf or NaN
+      }
+    }
+    const int64_t row = (int64_t(h) * c.slots_per_page + inner);
+    double s = 1.0;
+    if constexpr (TYPE == W4_KV_I8) {
+#pragma unroll
+      for (int o = kRowLanes / 2; o > 0; o /= 2) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        poison += __shfl_xor_sync(0xffffffffu, poison, o);
+      }
+      // the fp64 quotient rounded to fp32 is the correctly rounded fp32 one
+      const float sc = poison != 0.f ? __int_as_float(0x7fc00000) : (top > 0.f ? __fdiv_rn(top, 127.f) : 1.f);
+      // a scale that underflows to 0 stores zeros, which it also stands for
+      s = (poison != 0.f || sc == 0.f) ? static_cast<double>(INFINITY) : static_cast<double>(sc);
+      if (poison != 0.f) {
+#pragma unroll
+        for (int i = 0; i < kRowVecs; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      if (live && lane == 0)
+        (is_v ? c.vs : c.ks)[int64_t(page) * c.heads * c.slots_per_page + row] = sc;
+    }
+    if (!live) continue;
+    uint8_t* base = static_cast<uint8_t*>(is_v ? c.v : c.k) + int64_t(page) * c.page_stride * Elem<TYPE>::kBytes;
+#pragma unroll
+    for (int i = 0; i < kRowVecs; ++i) {
+      const int at = lane + i * kRowLanes;
+      if (at < vecs) store4<TYPE>(base, row * c.dim + 4 * at, x[i], s);
+    }
+  }
+}
+
+// The lengths advanced in place, once every row has been placed by the old ones.
+__global__ void __launch_bounds__(kThreads) advance_kernel(const AppendParams p, int32_t* lengths_out) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t b = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (b < p.c.seqs) lengths_out[b] = advanced(p, static_cast<int32_t>(b));
+}
+
+}  // namespace
+
+extern "C" w4_status kv_append(const kv_cache* c, const float* k, int64_t ldk, const float* v, int64_t ldv,
+                               const int32_t* cu_tokens, int64_t tokens, int32_t* lengths_out, void* stream) {
+  using namespace w4host;
+  AppendParams p = {};
+  w4_status rc = check_cache(c, "cache", &p.c);
+  if (rc != W4_OK) return rc;
+  const int64_t wide = int64_t(c->kv_heads) * c->head_dim;
+  if (tokens < 0 || tokens > 0x7fffffff) return fail(W4_ERR_SHAPE, "tokens=%lld is outside 0..2^31-1", (long long)tokens);
+  if (cu_tokens == nullptr && tokens != c->seqs)
+    return fail(W4_ERR_SHAPE, "without cu_tokens there is one row for each sequence: tokens=%lld, seqs=%lld",
+                (long long)tokens, (long long)c->seqs);
+  if (c->seqs == 0) return W4_OK;
+  if (c->ldp == 0 && c->seqs > 1 && tokens > 0)
+    return fail(W4_ERR_VALUE, "sequences that share one row of pages (ldp == 0) cannot be appended to");
+  if (lengths_out == nullptr) return fail(W4_ERR_NULL, "lengths_out is NULL");
+  if (tokens > 0 && (k == nullptr || v == nullptr)) return fail(W4_ERR_NULL, "k and v must not be NULL");
+  if (tokens > 1 && (ldk < wide || ldv < wide)) return fail(W4_ERR_SHAPE, "ldk and ldv must be at least kv_heads * head_dim");
+  const auto bits = [](const void* q) { return reinterpret_cast<uintptr_t>(q); };
+  if ((bits(k) | bits(v) | bits(cu_tokens) | bits(lengths_out)) & 3)
+    return fail(W4_ERR_ALIGN, "k, v, cu_tokens and lengths_out must be 4-byte aligned");
+  if (lengths_out != c->lengths) {
+    const uintptr_t a = bits(lengths_out), b = bits(c->lengths), n = static_cast<uintptr_t>(c->seqs) * 4;
+    if (a < b + n && b < a + n) return fail(W4_ERR_VALUE, "lengths_out overlaps the cache's lengths in part");
+  }
+  const DeviceInfo* di = nullptr;
+  rc = current_device(&di);
+  if (rc != W4_OK) return rc;
+  p.k = k;
+  p.v = v;
+  p.ldk = ldk;
+  p.ldv = ldv;
+  p.cu = cu_tokens;
+  p.tokens = tokens;
+  p.err = di->err;
+  p.vec = ((bits(k) | bits(v)) & 15) == 0 && (tokens <= 1 || ((ldk | ldv) & 3) == 0);
+  const bool in_place = cu_tokens != nullptr && lengths_out == c->lengths;
+  p.lengths_out = in_place ? nullptr : lengths_out;
+  const int64_t by_seq = (c->seqs + kThreads - 1) / kThreads;
+  const dim3 grid(static_cast<unsigned>(tokens > by_seq ? tokens : by_seq));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  switch (c->type) {
+    case W4_KV_F32: e = launch_pdl(append_kernel<W4_KV_F32>, grid, kThreads, 0, st, p); break;
+    case W4_KV_F16: e = launch_pdl(append_kernel<W4_KV_F16>, grid, kThreads, 0, st, p); break;
+    case W4_KV_BF16: e = launch_pdl(append_kernel<W4_KV_BF16>, grid, kThreads, 0, st, p); break;
+    default: e = launch_pdl(append_kernel<W4_KV_I8>, grid, kThreads, 0, st, p); break;
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "launch kv_append");
+  if (in_place) {
+    e = launch_pdl(advance_kernel, dim3(static_cast<unsigned>(by_seq)), kThreads, 0, st, p, lengths_out);
+    if (e != cudaSuccess) return cuda_fail(e, "launch kv_append (lengths)");
+  }
+  return W4_OK;
+}

@@ -1,0 +1,284 @@
+// kv_attend's host side, and the small kernels behind the attention kernels:
+// join_kernel (partials of items that several CTAs shared) and gather_kernel
+// (attention weights summed over the query heads).
+#include "kv_attend.cuh"
+
+namespace w4kv {
+
+template <>
+AttendKernel attend_kernel_for<W4_KV_F32>(int32_t dim, int32_t group);
+template <>
+AttendKernel attend_kernel_for<W4_KV_F16>(int32_t dim, int32_t group);
+template <>
+AttendKernel attend_kernel_for<W4_KV_BF16>(int32_t dim, int32_t group);
+template <>
+AttendKernel attend_kernel_for<W4_KV_I8>(int32_t dim, int32_t group);
+
+}  // namespace w4kv
+
+namespace {
+
+using namespace w4kv;
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kMaxLaneVecs = 2;  // float4s of a lane: 32 x 4 x 2 = 256, the largest head_dim
+
+// One query head per `wpr` warps: wpr = 8 spreads the partials of a few long
+// rows, wpr = 1 passes over many rows that mostly have nothing to join.
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p, int wpr) {
+  __shared__ float4 sm_a[kJoinWarps][32 * kMaxLaneVecs];
+  __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int q_heads = p.c.heads * p.group;
+  const int64_t row = int64_t(blockIdx.x) * (kJoinWarps / wpr) + warp / wpr;
+  const int sub = warp % wpr;
+  const int D = p.c.dim, vecs = D / 4;
+  float m = -INFINITY, l = 0.f;
+  float4 a[kMaxLaneVecs];
+#pragma unroll
+  for (int i = 0; i < kMaxLaneVecs; ++i) a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  bool work = false;
+  int32_t b = 0, qh = 0;
+  if (row < int64_t(p.c.seqs) * q_heads) {
+    b = static_cast<int32_t>(row / q_heads);
+    qh = static_cast<int32_t>(row % q_heads);
+    int32_t lo, n;
+    attended(p, b, lo, n);
+    int2 meta = make_int2(0, 0);
+    const int32_t h = qh / p.group, g = (qh % p.group) % p.rows;
+    if (n > lo) meta = p.meta[(int64_t(b) * p.c.heads + h) * p.chunks + (qh % p.group) / p.rows];
+    work = meta.y != 1;
+    for (int32_t i = sub; i < (work ? meta.y : 0); i += wpr) {
+      // the first partial, then the next CTAs' first ones
+      const int64_t slot = i == 0 ? meta.x : 2 * int64_t(meta.x / 2 + i);
+      const float* part = p.part + slot * p.part_stride;
+      const float pm = part[p.rows * D + g], pl = part[p.rows * D + p.rows + g];
+      const float top = fmaxf(m, pm);
+      const float f = m == -INFINITY ? 1.f : ex2(m - top), pf = pm == -INFINITY ? 1.f : ex2(pm - top);
+      m = top;
+      l = l * f + pl * pf;
+#pragma unroll
+      for (int j = 0; j < kMaxLaneVecs; ++j) {
+        if (lane + 32 * j < vecs) {
+          const float4 x = *reinterpret_cast<const float4*>(part + g * D + 4 * (lane + 32 * j));
+          a[j] = make_float4(a[j].x * f + x.x * pf, a[j].y * f + x.y * pf, a[j].z * f + x.z * pf,
+                             a[j].w * f + x.w * pf);
+        }
+      }
+    }
+  }
+  if (wpr > 1) {
+    if (lane == 0) {
+      sm_m[warp] = m;
+      sm_l[warp] = l;
+    }
+#pragma unroll
+    for (int j = 0; j < kMaxLaneVecs; ++j) sm_a[warp][lane + 32 * j] = a[j];
+    __syncthreads();
+    if (sub != 0) return;
+    for (int w = warp + 1; w < warp + wpr; ++w) {
+      const float pm = sm_m[w];
+      const float top = fmaxf(m, pm);
+      const float f = m == -INFINITY ? 1.f : ex2(m - top), pf = pm == -INFINITY ? 1.f : ex2(pm - top);
+      m = top;
+      l = l * f + sm_l[w] * pf;
+#pragma unroll
+      for (int j = 0; j < kMaxLaneVecs; ++j) {
+        const float4 x = sm_a[w][lane + 32 * j];
+        a[j] = make_float4(a[j].x * f + x.x * pf, a[j].y * f + x.y * pf, a[j].z * f + x.z * pf, a[j].w * f + x.w * pf);
+      }
+    }
+  }
+  if (!work) return;
+  const bool none = l == 0.f;
+#pragma unroll
+  for (int j = 0; j < kMaxLaneVecs; ++j) {
+    if (lane + 32 * j < vecs) {
+      float* o = p.out + b * p.ldo + int64_t(qh) * D + 4 * (lane + 32 * j);
+      o[0] = none ? 0.f : a[j].x / l;
+      o[1] = none ? 0.f : a[j].y / l;
+      o[2] = none ? 0.f : a[j].z / l;
+      o[3] = none ? 0.f : a[j].w / l;
+    }
+  }
+  if (lane == 0) {
+    const float z = none ? -INFINITY : m + log2f(l);
+    if (p.lse != nullptr) p.lse[row] = z * kLn2;
+    if (p.lse2 != nullptr) p.lse2[row] = z;
+  }
+}
+
+// acc[b, j] += sum over the query heads of 2^(x - lse2), heads in order.
+__global__ void __launch_bounds__(kJoinThreads) gather_kernel(const AttendParams p, float* acc, int64_t ldacc) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int32_t b = blockIdx.y;
+  const int q_heads = p.c.heads * p.group;
+  int32_t lo, n;
+  attended(p, b, lo, n);
+  const float* z = p.lse2 + int64_t(b) * q_heads;
+  for (int64_t j = lo + int64_t(blockIdx.x) * kJoinThreads + threadIdx.x; j < n; j += int64_t(gridDim.x) * kJoinThreads) {
+    const float* x = p.scores + int64_t(b) * q_heads * p.c.capacity + j;
+    float sum = 0.f;
+    for (int i = 0; i < q_heads; ++i) {
+      const float zi = z[i];  // -Inf: every attended score is -Inf, and weighs nothing
+      sum += zi == -INFINITY ? 0.f : ex2(x[int64_t(i) * p.c.capacity] - zi);
+    }
+    acc[int64_t(b) * ldacc + j] += sum;
+  }
+}
+
+struct Layout {
+  AttendKernel kernel;
+  size_t smem;
+  int32_t chunks;
+  unsigned ctas;
+  int64_t part_stride;
+  size_t meta, lse2, scores, bytes;  // offsets, and the total
+};
+
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+AttendKernel choose(const w4kv::View& c, int type, int32_t group) {
+  switch (type) {
+    case W4_KV_F32: return attend_kernel_for<W4_KV_F32>(c.dim, group);
+    case W4_KV_F16: return attend_kernel_for<W4_KV_F16>(c.dim, group);
+    case W4_KV_BF16: return attend_kernel_for<W4_KV_BF16>(c.dim, group);
+    default: return attend_kernel_for<W4_KV_I8>(c.dim, group);
+  }
+}
+
+// CTAs of a kernel that an SM holds (asked once for each kernel and head_dim).
+w4_status resident(const AttendKernel& k, size_t smem, int* out) {
+  struct Known {
+    const void* fn;
+    size_t smem;
+    int n;
+  };
+  static thread_local Known known[16] = {};
+  static thread_local int next = 0;
+  const void* fn = reinterpret_cast<const void*>(k.fn);
+  for (const Known& e : known)
+    if (e.fn == fn && e.smem == smem) {
+      *out = e.n;
+      return W4_OK;
+    }
+  int n = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k.fn, kAttendThreads, smem);
+  if (e != cudaSuccess) return w4host::cuda_fail(e, "kv_attend occupancy");
+  if (n < 1) return w4host::fail(W4_ERR_CUDA, "kv_attend: no CTA fits an SM");
+  known[next] = {fn, smem, n};
+  next = (next + 1) % 16;
+  *out = n;
+  return W4_OK;
+}
+
+w4_status lay_out(const w4kv::View& c, int type, int64_t q_heads, bool with_acc, int sms, Layout* out) {
+  const int32_t group = static_cast<int32_t>(q_heads / c.heads);
+  Layout L = {};
+  L.kernel = choose(c, type, group);
+  L.chunks = (group + L.kernel.rows - 1) / L.kernel.rows;
+  L.smem = (static_cast<size_t>(kWarps) * L.kernel.rows * (c.dim + 2) + L.kernel.body_floats) * 4;
+  int per_sm = 0;
+  const w4_status rc = resident(L.kernel, L.smem, &per_sm);
+  if (rc != W4_OK) return rc;
+  const int64_t items = int64_t(c.seqs) * c.heads * L.chunks;
+  const int64_t most = items * ((c.capacity + kUnit - 1) / kUnit);
+  L.ctas = static_cast<unsigned>(most < int64_t(per_sm) * sms ? (most > 0 ? most : 1) : int64_t(per_sm) * sms);
+  L.part_stride = (int64_t(L.kernel.rows) * (c.dim + 2) + 3) / 4 * 4;
+  L.meta = round256(size_t(2) * L.ctas * L.part_stride * 4);
+  L.lse2 = L.meta + round256(static_cast<size_t>(items) * sizeof(int2));
+  L.scores = L.lse2 + (with_acc ? round256(static_cast<size_t>(c.seqs) * q_heads * 4) : 0);
+  L.bytes = L.scores + (with_acc ? static_cast<size_t>(c.seqs) * q_heads * c.capacity * 4 : 0);
+  *out = L;
+  return W4_OK;
+}
+
+w4_status check_heads(const w4kv::View& c, int64_t q_heads) {
+  if (q_heads < 1 || q_heads > (1 << 20) || q_heads % c.heads != 0)
+    return w4host::fail(W4_ERR_SHAPE, "q_heads=%lld is not a multiple of kv_heads=%d", (long long)q_heads, int(c.heads));
+  return W4_OK;
+}
+
+}  // namespace
+
+extern "C" size_t kv_attend_workspace_size(const kv_cache* c, int64_t q_heads, int32_t with_acc) {
+  using namespace w4host;
+  w4kv::View v;
+  const DeviceInfo* di = nullptr;
+  Layout L;
+  if (check_cache(c, "cache", &v) != W4_OK || check_heads(v, q_heads) != W4_OK || c->seqs == 0 ||
+      current_device(&di) != W4_OK || lay_out(v, c->type, q_heads, with_acc != 0, di->sms, &L) != W4_OK)
+    return 0;
+  return L.bytes;
+}
+
+extern "C" w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, int64_t q_heads, float scale,
+                               int64_t window, float* out, int64_t ldo, float* lse, float* acc, int64_t ldacc,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace w4host;
+  AttendParams p = {};
+  w4_status rc = check_cache(c, "cache", &p.c);
+  if (rc != W4_OK) return rc;
+  rc = check_heads(p.c, q_heads);
+  if (rc != W4_OK) return rc;
+  if (window < 0) return fail(W4_ERR_VALUE, "window=%lld is negative", (long long)window);
+  if (!(scale > -INFINITY && scale < INFINITY)) return fail(W4_ERR_VALUE, "scale is not finite");
+  if (c->seqs == 0) return W4_OK;
+  if (q == nullptr || out == nullptr) return fail(W4_ERR_NULL, "q and out must not be NULL");
+  if (c->seqs > 1 && (ldq < q_heads * c->head_dim || ldo < q_heads * c->head_dim))
+    return fail(W4_ERR_SHAPE, "ldq and ldo must be at least q_heads * head_dim");
+  if (acc != nullptr && c->seqs > 1 && ldacc < p.c.capacity)
+    return fail(W4_ERR_SHAPE, "ldacc=%lld is below the capacity of %d slots", (long long)ldacc, int(p.c.capacity));
+  const auto bits = [](const void* x) { return reinterpret_cast<uintptr_t>(x); };
+  if ((bits(q) | bits(out) | bits(lse) | bits(acc)) & 3)
+    return fail(W4_ERR_ALIGN, "q, out, lse and acc must be 4-byte aligned");
+  const DeviceInfo* di = nullptr;
+  rc = current_device(&di);
+  if (rc != W4_OK) return rc;
+  Layout L;
+  rc = lay_out(p.c, c->type, q_heads, acc != nullptr, di->sms, &L);
+  if (rc != W4_OK) return rc;
+  if (workspace == nullptr || workspace_bytes < L.bytes)
+    return fail(W4_ERR_WORKSPACE, "kv_attend needs a workspace of %zu bytes, %zu given", L.bytes,
+                workspace == nullptr ? size_t(0) : workspace_bytes);
+  if (bits(workspace) & 15) return fail(W4_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.q = q;
+  p.ldq = ldq;
+  p.out = out;
+  p.ldo = ldo;
+  p.lse = lse;
+  p.part = reinterpret_cast<float*>(ws);
+  p.meta = reinterpret_cast<int2*>(ws + L.meta);
+  if (acc != nullptr) {
+    p.lse2 = reinterpret_cast<float*>(ws + L.lse2);
+    p.scores = reinterpret_cast<float*>(ws + L.scores);
+  }
+  p.part_stride = L.part_stride;
+  p.window = window;
+  p.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  p.group = static_cast<int32_t>(q_heads / c->kv_heads);
+  p.rows = L.kernel.rows;
+  p.chunks = L.chunks;
+  p.err = di->err;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_pdl(L.kernel.fn, dim3(L.ctas), kAttendThreads, L.smem, st, p);
+  if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend");
+  const int64_t rows = c->seqs * q_heads;
+  const int wpr = rows <= int64_t(di->sms) * kJoinWarps ? kJoinWarps : 1;
+  const int64_t rows_per_cta = kJoinWarps / wpr;
+  e = launch_pdl(join_kernel, dim3(static_cast<unsigned>((rows + rows_per_cta - 1) / rows_per_cta)), kJoinThreads, 0, st,
+                 p, wpr);
+  if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend (join)");
+  if (acc != nullptr && p.c.capacity > 0) {
+    const int64_t per_row = (p.c.capacity + kJoinThreads - 1) / kJoinThreads;
+    const dim3 grid(static_cast<unsigned>(per_row < 512 ? per_row : 512), static_cast<unsigned>(c->seqs));
+    e = launch_pdl(gather_kernel, grid, kJoinThreads, 0, st, p, acc, ldacc);
+    if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend (weights)");
+  }
+  return W4_OK;
+}

@@ -1,0 +1,303 @@
+"""GPU parity of kv_attend against the fp64 definition: element types, head
+layouts, page sizes, lengths from none to several splits, windows, strides,
+gathered weights, graphs, streams and broken descriptors."""
+
+import numpy as np
+import pytest
+
+import oracle
+from kv_util import KINDS, build, clear_error, error_status, torch, w4
+
+pytestmark = pytest.mark.gpu
+
+
+def check(cache, rows_k, rows_v, q, window=0, scale=None, with_acc=False, strided=False, what=""):
+    T = torch()
+    B, Hq, D = q.shape
+    clear_error()
+    scale = D ** -0.5 if scale is None else scale
+    if strided:  # q and out as columns of wider rows, the columns around out untouched
+        wide = T.full((B, Hq * D + 40), float("nan"), device="cuda")
+        wide[:, 8:8 + Hq * D] = T.from_numpy(q.reshape(B, -1)).cuda()
+        qd = wide[:, 8:8 + Hq * D].view(B, Hq, D)
+        obuf = T.full((B, Hq * D + 12), 7.0, device="cuda")
+        out = obuf[:, 4:4 + Hq * D].view(B, Hq, D)
+    else:
+        qd, out = T.from_numpy(q).cuda(), T.full((B, Hq, D), float("nan"), device="cuda")
+    lse = T.full((B, Hq), float("nan"), device="cuda")
+    acc = acc0 = None
+    if with_acc:
+        acc0 = np.random.default_rng(5).random((B, cache.capacity + 3)).astype(np.float32)
+        acc = T.from_numpy(acc0).cuda()
+    w4().kv_attend(qd, cache, scale=scale, window=window, out=out, lse=lse, acc=acc)
+    assert error_status() == 0, what
+    got, gl = out.cpu().double().numpy(), lse.cpu().double().numpy()
+    for b in range(B):
+        ro, rl, rw, (to, tl, tw) = oracle.kv_attend_ref(q[b], rows_k[b], rows_v[b], scale, window)
+        off = np.abs(got[b] - ro)
+        assert np.all(off <= to), f"{what} seq {b}: out off by {np.nanmax(off / np.maximum(to, 1e-300)):.3g} bounds"
+        if len(rows_k[b]) == 0:
+            assert np.all(gl[b] == -np.inf)
+        else:
+            assert np.all(np.abs(gl[b] - rl) <= tl), (what, b, np.abs(gl[b] - rl).max(), tl.max())
+        if with_acc:
+            ga, n = acc[b].cpu().double().numpy(), rw.shape[1]
+            want = acc0[b].astype(np.float64)
+            assert np.array_equal(ga[n:], want[n:]), f"{what} seq {b}: weights behind the last slot changed"
+            full = want[:n] + rw.sum(0)
+            tol = tw.sum(0) + (Hq + 1) * oracle.EPS * full
+            assert np.all(np.abs(ga[:n] - full) <= tol), (what, b)
+    if strided:
+        o = obuf.cpu().numpy()
+        assert np.all(o[:, :4] == 7.0) and np.all(o[:, 4 + Hq * D:] == 7.0)
+    return out
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("heads,group,dim,page", [
+    (12, 1, 64, 16), (3, 1, 96, 7), (2, 2, 128, 32), (2, 3, 48, 5), (1, 4, 128, 64), (2, 8, 64, 16), (1, 5, 80, 1),
+    (1, 16, 32, 3), (2, 7, 112, 33), (1, 1, 256, 16), (1, 9, 256, 20), (2, 1, 16, 4), (1, 4, 192, 8), (1, 6, 96, 16),
+    (1, 2, 160, 16), (1, 12, 128, 16),
+])
+def test_attend_matches_the_definition(kind, heads, group, dim, page):
+    rng = np.random.default_rng(heads * 1000 + group * 100 + dim + page)
+    lengths = [0, 1, 2, 15, 16, 17, 63, 64, 65, 130, 301]
+    cache, k, v = build(rng, kind, lengths, heads, dim, page)
+    q = rng.standard_normal((len(lengths), heads * group, dim)).astype(np.float32)
+    check(cache, k, v, q, with_acc=True, strided=True, what=f"{kind} {heads}x{group}x{dim}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window", [1, 5, 64, 100, 5000])
+def test_attend_window(kind, window):
+    rng = np.random.default_rng(window)
+    lengths = [0, 1, 99, 100, 101, 333, 700]
+    cache, k, v = build(rng, kind, lengths, 2, 64, 16)
+    q = rng.standard_normal((len(lengths), 4, 64)).astype(np.float32)
+    check(cache, k, v, q, window=window, with_acc=True, what=f"window {window}")
+
+
+@pytest.mark.parametrize("kind,heads,group,dim,n", [
+    ("float32", 1, 1, 64, 20011), ("bfloat16", 2, 4, 128, 30000), ("int8", 1, 8, 128, 40003), ("float16", 1, 1, 96, 9001),
+])
+def test_attend_one_long_sequence_is_split_and_joined(kind, heads, group, dim, n):
+    rng = np.random.default_rng(n)
+    cache, k, v = build(rng, kind, [n], heads, dim, 64)
+    q = (rng.standard_normal((1, heads * group, dim)) * 2).astype(np.float32)
+    check(cache, k, v, q, with_acc=True, what=f"{kind} {n}")
+
+
+@pytest.mark.parametrize("kind", ["float32", "int8"])
+def test_attend_many_sequences(kind):
+    """More sequences than one pass of the run search takes, some empty."""
+    rng = np.random.default_rng(17)
+    lengths = [int(x) for x in rng.integers(0, 90, 300)]
+    lengths[0] = lengths[127] = lengths[128] = lengths[299] = 0
+    cache, k, v = build(rng, kind, lengths, 2, 64, 16)
+    q = rng.standard_normal((300, 4, 64)).astype(np.float32)
+    check(cache, k, v, q, what="300 sequences")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attend_large_scores_and_values(kind):
+    """Scores of +-100 and more, values of very different magnitude: the
+    running maximum rescales, and each rescaling keeps its precision."""
+    rng = np.random.default_rng(3)
+    for heads, group in ((2, 1), (1, 8)):
+        cache, k, v = build(rng, kind, [257, 64, 1000], heads, 64, 16, amp=6.0)
+        q = (rng.standard_normal((3, heads * group, 64)) * 5).astype(np.float32)
+        check(cache, k, v, q, scale=0.3, with_acc=True, what="large scores")
+        check(cache, k, v, q, scale=-0.3, what="negative scale")
+        check(cache, k, v, q, scale=0.0, what="zero scale: the mean of the values")
+        check(cache, k, v, (q * 1e-30).astype(np.float32), what="tiny queries")
+        check(cache, k, v, (q * 0).astype(np.float32), what="zero queries")
+
+
+def test_attend_int8_scales_of_any_size():
+    """int8 rows whose scales span 1e-6 .. 1e5, zero scales among them."""
+    T = torch()
+    rng = np.random.default_rng(8)
+    for group in (1, 8):
+        lengths = [100, 700]
+        cache, k, v = build(rng, "int8", lengths, 2, 64, 16)
+        for t in (cache.k_scales, cache.v_scales):
+            f = T.from_numpy((10.0 ** rng.uniform(-6, 5, tuple(t.shape))).astype(np.float32)).cuda()
+            t.mul_(f if t is cache.v_scales else f.clamp(max=10.0))
+            t[:, :, 0] *= 0.0
+        # slot 0 of a page that no sequence holds is NaN * 0 and stays NaN
+        from kv_util import read_rows
+        rows = [read_rows(cache, b, n) for b, n in enumerate(lengths)]
+        q = rng.standard_normal((2, 2 * group, 64)).astype(np.float32)
+        check(cache, [r[0] for r in rows], [r[1] for r in rows], q, with_acc=True, what="scales")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attend_pages_far_apart_and_shared(kind):
+    """Pages with others between them, and one row of pages that "sequences"
+    of lengths 1 .. T share: a prompt attended causally."""
+    rng = np.random.default_rng(23)
+    cache, k, v = build(rng, kind, [77, 130], 2, 64, 16, gap=2)
+    q = rng.standard_normal((2, 2, 64)).astype(np.float32)
+    check(cache, k, v, q, what="gaps")
+    T_len = 58
+    cache, k, v = build(rng, kind, list(range(1, T_len + 1)), 2, 64, 16, shared=True)
+    assert cache.page_table.stride(0) == 0
+    q = rng.standard_normal((T_len, 4, 64)).astype(np.float32)
+    check(cache, k, v, q, with_acc=True, what="causal prompt")
+
+
+def test_attend_offsets_beyond_32_bits():
+    """Pages whose elements lie more than 2^32 elements (and bytes) in."""
+    T = torch()
+    rng = np.random.default_rng(31)
+    H, S, D = 2, 16, 64
+    page = H * S * D
+    far = (1 << 32) // page + 5
+    k = T.empty((far + 1, H, S, D), dtype=T.float16, device="cuda")
+    v = T.empty((far + 1, H, S, D), dtype=T.float16, device="cuda")
+    x = rng.standard_normal((2, S, H, D)).astype(np.float16)
+    ids = [far, 1]
+    for i, p in enumerate(ids):
+        k[p].copy_(T.from_numpy(np.ascontiguousarray(x[i].transpose(1, 0, 2))).cuda())
+        v[p].copy_(T.from_numpy(np.ascontiguousarray(x[1 - i].transpose(1, 0, 2))).cuda())
+    cache = w4().KvCache(k, v, T.tensor([ids], dtype=T.int32, device="cuda"), T.tensor([30], dtype=T.int32, device="cuda"))
+    rows_k = x.reshape(32, H, D)[:30].astype(np.float64)
+    rows_v = x[::-1].reshape(32, H, D)[:30].astype(np.float64)
+    for group in (1, 8):
+        q = rng.standard_normal((1, H * group, D)).astype(np.float32)
+        check(cache, [rows_k], [rows_v], q, with_acc=True, what="far pages")
+
+
+@pytest.mark.parametrize("kind,group", [("float32", 1), ("bfloat16", 4), ("int8", 8), ("float16", 8)])
+def test_attend_nan_reaches_only_its_own_rows(kind, group):
+    """A NaN in q, or Inf and NaN in an attended slot, makes the rows that it
+    reaches non-finite and leaves every other row's bits as they were."""
+    T = torch()
+    rng = np.random.default_rng(41)
+    cache, k, v = build(rng, kind, [150, 90, 33], 2, 64, 16)
+    q = rng.standard_normal((3, 2 * group, 64)).astype(np.float32)
+    base = check(cache, k, v, q, what="clean").cpu().numpy()
+    bad = q.copy()
+    bad[1, 0, 5] = np.nan
+    out = w4().kv_attend(T.from_numpy(bad).cuda(), cache).cpu().numpy()
+    assert np.all(np.isnan(out[1, 0]))
+    keep = np.ones((3, 2 * group), bool)
+    keep[1, 0] = False
+    assert np.array_equal(out[keep], base[keep])
+    p = int(cache.page_table[0, 2])
+    if kind == "int8":
+        cache.v_scales[p, 1, 3] = float("nan")
+    else:
+        cache.v[p, 1, 3, :] = float("inf")
+    out = w4().kv_attend(T.from_numpy(q).cuda(), cache).cpu().numpy()
+    assert not np.any(np.isfinite(out[0, group:]))
+    assert np.array_equal(out[0, :group], base[0, :group]) and np.array_equal(out[1:], base[1:])
+
+
+def test_attend_broken_pages_and_lengths_are_recorded():
+    """A page id that names no page, and lengths outside the capacity: the
+    error word says so, the slots concerned count as empty."""
+    T = torch()
+    rng = np.random.default_rng(51)
+    for kind, group in (("float32", 1), ("bfloat16", 4), ("int8", 8)):
+        cache, k, v = build(rng, kind, [40, 48], 2, 64, 16)
+        q = rng.standard_normal((2, 2 * group, 64)).astype(np.float32)
+        qd = T.from_numpy(q).cuda()
+        clear_error()
+        good = int(cache.page_table[0, 1])
+        for broken in (-1, cache.k.shape[0], 2 ** 31 - 1):
+            cache.page_table[0, 1] = broken
+            out = w4().kv_attend(qd, cache).cpu().double().numpy()
+            assert error_status() == 8
+            j = np.r_[0:16, 32:40]
+            ro, _, _, (to, _, _) = oracle.kv_attend_ref(q[0], k[0][j], v[0][j], 0.125)
+            assert np.all(np.abs(out[0] - ro) <= to)
+        cache.page_table[0, 1] = good
+        cache.lengths.copy_(T.tensor([-5, 49], dtype=T.int32))
+        out = w4().kv_attend(qd, cache).cpu().double().numpy()
+        assert error_status() == 8
+        assert np.all(out[0] == 0)
+        ro, _, _, (to, _, _) = oracle.kv_attend_ref(q[1], k[1], v[1], 0.125)
+        assert np.all(np.abs(out[1] - ro) <= to)
+
+
+@pytest.mark.parametrize("kind,group", [("float32", 1), ("float16", 4)])
+def test_attend_in_a_graph_follows_the_lengths(kind, group):
+    """A captured call is replayed while the lengths change, two captured
+    calls are replayed on two streams at once, and every result is bit for bit
+    what an eager call gives."""
+    T = torch()
+    rng = np.random.default_rng(61)
+    cache, k, v = build(rng, kind, [500, 3, 260], 2, 64, 16)
+    q = T.from_numpy(rng.standard_normal((3, 2 * group, 64)).astype(np.float32)).cuda()
+    q2 = T.from_numpy(rng.standard_normal((3, 2 * group, 64)).astype(np.float32)).cuda()
+    w4().kv_attend(q, cache)
+    T.cuda.synchronize()
+    graphs = []
+    for x in (q, q2):
+        g = T.cuda.CUDAGraph()
+        with T.cuda.graph(g):
+            out = w4().kv_attend(x, cache)
+        graphs.append((g, out))
+    streams = [T.cuda.Stream(), T.cuda.Stream()]
+    for lengths in ([500, 3, 260], [1, 0, 0], [0, 0, 0], [499, 2, 17]):
+        cache.lengths.copy_(T.tensor(lengths, dtype=T.int32))
+        T.cuda.synchronize()
+        for _ in range(20):
+            for (g, _), s in zip(graphs, streams):
+                with T.cuda.stream(s):
+                    g.replay()
+        T.cuda.synchronize()
+        for (g, out), x in zip(graphs, (q, q2)):
+            assert T.equal(out, w4().kv_attend(x, cache))
+
+
+def test_attend_on_a_stream_of_its_own():
+    T = torch()
+    rng = np.random.default_rng(71)
+    cache, k, v = build(rng, "bfloat16", [300, 200], 2, 64, 16)
+    q = T.from_numpy(rng.standard_normal((2, 2, 64)).astype(np.float32)).cuda()
+    want = w4().kv_attend(q, cache)
+    T.cuda.synchronize()
+    s = T.cuda.Stream()
+    outs = [w4().kv_attend(q, cache, stream=s) for _ in range(50)]
+    mine = [w4().kv_attend(q, cache) for _ in range(50)]
+    T.cuda.synchronize()
+    assert all(T.equal(o, want) for o in outs + mine)
+
+
+def test_attend_no_sequences_and_no_capacity():
+    T = torch()
+    k = T.zeros((1, 2, 16, 64), device="cuda")
+    none = w4().KvCache(k, k.clone(), T.zeros((0, 3), dtype=T.int32, device="cuda"),
+                        T.zeros(0, dtype=T.int32, device="cuda"))
+    assert w4().kv_attend(T.zeros((0, 4, 64), device="cuda"), none).shape == (0, 4, 64)
+    flat = w4().KvCache(k, k.clone(), T.zeros((2, 0), dtype=T.int32, device="cuda"),
+                        T.zeros(2, dtype=T.int32, device="cuda"))
+    out = w4().kv_attend(T.ones((2, 4, 64), device="cuda"), flat, acc=T.zeros((2, 0), device="cuda"))
+    assert T.count_nonzero(out) == 0 and error_status() == 0
+
+
+def test_attend_refusals():
+    T = torch()
+    rng = np.random.default_rng(81)
+    cache, _, _ = build(rng, "float32", [40, 48], 2, 64, 16)
+    q = T.zeros((2, 4, 64), device="cuda")
+    for bad in (q[:1], q.half(), q[:, :, :32], q.cpu(), T.zeros((2, 4, 128), device="cuda")[:, :, ::2]):
+        with pytest.raises(ValueError):
+            w4().kv_attend(bad, cache)
+    with pytest.raises(w4().W4Error):
+        w4().kv_attend(T.zeros((2, 3, 64), device="cuda"), cache)  # 3 query heads over 2
+    with pytest.raises(w4().W4Error):
+        w4().kv_attend(q, cache, window=-1)
+    with pytest.raises(w4().W4Error):
+        w4().kv_attend(q, cache, scale=float("nan"))
+    with pytest.raises(w4().W4Error) as e:
+        w4().kv_attend(q, cache, ws=T.empty(16, dtype=T.uint8, device="cuda"))
+    assert e.value.status == 7
+    with pytest.raises(ValueError):
+        w4().kv_attend(q, cache, lse=T.zeros((2, 2), device="cuda"))
+    with pytest.raises(ValueError):
+        w4().kv_attend(q, cache, acc=T.zeros((2, 47), device="cuda"))
+    with pytest.raises(ValueError):
+        w4().kv_attend(q, cache, out=T.zeros((2, 4, 64), device="cuda").half())

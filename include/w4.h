@@ -548,8 +548,9 @@ typedef enum w4_kv_type { W4_KV_F32 = 0, W4_KV_F16 = 1, W4_KV_BF16 = 2, W4_KV_I8
 /* One layer's paged cache. All arrays are the caller's device memory.
  * - k, v: [num_pages] pages of [kv_heads][page_size][head_dim] elements, pages
  *   page_stride elements apart (page_stride >= kv_heads * page_size *
- *   head_dim, a multiple of 16 bytes); 16-byte aligned. head_dim is a
- *   multiple of 16, at most 256; page_size is any number from 1 to 65536.
+ *   head_dim, a multiple of head_dim; num_pages * page_stride is below 2^32
+ *   rows of head_dim elements); 16-byte aligned. head_dim is a multiple of 16,
+ *   at most 256; page_size is any number from 1 to 65536.
  * - k_scales, v_scales: W4_KV_I8 only (NULL otherwise): fp32 [num_pages]
  *   [kv_heads][page_size], packed, 4-byte aligned.
  * - page_table: int32, row b (at b * ldp) names the pages of sequence b in
@@ -614,6 +615,7 @@ W4_API w4_status kv_append(const kv_cache* c, const float* k, int64_t ldk, const
  * - workspace: kv_attend_workspace_size() bytes of device memory, 16-byte
  *   aligned; needs no zeroing and holds nothing between calls. Calls that may
  *   run at the same time must not share it.
+ * - seqs * kv_heads * ceil(group / 4) * capacity must be below 2^36.
  * Sums and the softmax are fp32; K and V enter with their stored values. A
  * NaN or Inf in q or in an attended slot makes the rows that it reaches
  * non-finite; what lies in other slots has no effect. Results do not depend

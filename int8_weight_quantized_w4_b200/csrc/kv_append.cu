@@ -22,11 +22,12 @@ w4_status check_cache(const kv_cache* c, const char* what, w4kv::View* out) {
     return fail(W4_ERR_SHAPE, "%s: num_pages must be below 2^31 and seqs at most 65535", what);
   if (c->max_pages > (int64_t(1) << 30) / c->page_size)
     return fail(W4_ERR_SHAPE, "%s: max_pages * page_size is above 2^30", what);
-  const int64_t es = w4kv::elem_bytes(c->type);
   const int64_t page = int64_t(c->kv_heads) * c->page_size * c->head_dim;
-  if (c->page_stride < page || c->page_stride > (int64_t(1) << 40) || c->page_stride * es % 16 != 0)
-    return fail(W4_ERR_SHAPE, "%s: page_stride=%lld is below a page's %lld elements or no multiple of 16 bytes", what,
+  if (c->page_stride < page || c->page_stride > (int64_t(1) << 40) || c->page_stride % c->head_dim != 0)
+    return fail(W4_ERR_SHAPE, "%s: page_stride=%lld is below a page's %lld elements or no multiple of head_dim", what,
                 (long long)c->page_stride, (long long)page);
+  if (c->num_pages * (c->page_stride / c->head_dim) > 0xFFFFFFFFll)
+    return fail(W4_ERR_SHAPE, "%s: num_pages * page_stride is above 2^32 rows of head_dim elements", what);
   if (c->ldp != 0 && c->ldp < c->max_pages) return fail(W4_ERR_SHAPE, "%s: ldp=%lld < max_pages", what, (long long)c->ldp);
   if (c->seqs > 0) {
     if (c->lengths == nullptr) return fail(W4_ERR_NULL, "%s: lengths is NULL", what);
@@ -53,6 +54,11 @@ w4_status check_cache(const kv_cache* c, const char* what, w4kv::View* out) {
   out->seqs = static_cast<int32_t>(c->seqs);
   out->heads = c->kv_heads;
   out->slots_per_page = c->page_size;
+  out->page_rows = static_cast<uint32_t>(c->page_stride / c->head_dim);
+  const uint32_t d = static_cast<uint32_t>(c->page_size);
+  uint32_t l = 0;
+  while ((1u << l) < d) ++l;
+  out->page = {d, static_cast<uint32_t>(((uint64_t((1u << l) - d) << 32) / d) + 1), l};
   out->dim = c->head_dim;
   out->capacity = static_cast<int32_t>(c->max_pages * c->page_size);
   return W4_OK;
@@ -165,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     if (threadIdx.x == 0) w4dev::record_error(p.err, W4_ERR_VALUE, w4dev::K_KV_APPEND, b);
     return;
   }
-  const int32_t page = page_of(c, b, slot / c.slots_per_page, p.err, w4dev::K_KV_APPEND);
+  const int32_t page = page_of(c, b, c.page.quotient(slot), p.err, w4dev::K_KV_APPEND);
   if (page < 0) return;
   const int32_t inner = slot % c.slots_per_page;
   const int lane = threadIdx.x % kRowLanes;

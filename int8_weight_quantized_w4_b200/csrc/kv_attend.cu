@@ -133,7 +133,6 @@ __global__ void __launch_bounds__(kJoinThreads) gather_kernel(const AttendParams
 
 struct Layout {
   AttendKernel kernel;
-  size_t smem;
   int32_t chunks;
   unsigned ctas;
   int64_t part_stride;
@@ -151,26 +150,27 @@ AttendKernel choose(const w4kv::View& c, int type, int32_t group) {
   }
 }
 
-// CTAs of a kernel that an SM holds (asked once for each kernel and head_dim).
-w4_status resident(const AttendKernel& k, size_t smem, int* out) {
+// CTAs of a kernel that an SM holds (asked once for each kernel).
+w4_status resident(const AttendKernel& k, int* out) {
   struct Known {
     const void* fn;
-    size_t smem;
     int n;
   };
   static thread_local Known known[16] = {};
   static thread_local int next = 0;
   const void* fn = reinterpret_cast<const void*>(k.fn);
   for (const Known& e : known)
-    if (e.fn == fn && e.smem == smem) {
+    if (e.fn == fn) {
       *out = e.n;
       return W4_OK;
     }
   int n = 0;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k.fn, kAttendThreads, smem);
+  cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
+  if (e != cudaSuccess) return w4host::cuda_fail(e, "kv_attend shared memory");
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k.fn, kAttendThreads, k.smem);
   if (e != cudaSuccess) return w4host::cuda_fail(e, "kv_attend occupancy");
   if (n < 1) return w4host::fail(W4_ERR_CUDA, "kv_attend: no CTA fits an SM");
-  known[next] = {fn, smem, n};
+  known[next] = {fn, n};
   next = (next + 1) % 16;
   *out = n;
   return W4_OK;
@@ -181,12 +181,12 @@ w4_status lay_out(const w4kv::View& c, int type, int64_t q_heads, bool with_acc,
   Layout L = {};
   L.kernel = choose(c, type, group);
   L.chunks = (group + L.kernel.rows - 1) / L.kernel.rows;
-  L.smem = (static_cast<size_t>(kWarps) * L.kernel.rows * (c.dim + 2) + L.kernel.body_floats) * 4;
   int per_sm = 0;
-  const w4_status rc = resident(L.kernel, L.smem, &per_sm);
+  const w4_status rc = resident(L.kernel, &per_sm);
   if (rc != W4_OK) return rc;
   const int64_t items = int64_t(c.seqs) * c.heads * L.chunks;
-  const int64_t most = items * ((c.capacity + kUnit - 1) / kUnit);
+  const int64_t most = items * ((c.capacity + L.kernel.unit - 1) / L.kernel.unit + kOver);
+  if (most > 0x7fffffff) return w4host::fail(W4_ERR_SHAPE, "seqs x heads x capacity are more slots than a call takes");
   L.ctas = static_cast<unsigned>(most < int64_t(per_sm) * sms ? (most > 0 ? most : 1) : int64_t(per_sm) * sms);
   L.part_stride = (int64_t(L.kernel.rows) * (c.dim + 2) + 3) / 4 * 4;
   L.meta = round256(size_t(2) * L.ctas * L.part_stride * 4);
@@ -263,10 +263,12 @@ extern "C" w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, i
   p.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.group = static_cast<int32_t>(q_heads / c->kv_heads);
   p.rows = L.kernel.rows;
+  while ((1 << p.unit_log) < L.kernel.unit) ++p.unit_log;
+  p.q_vec = (bits(q) & 15) == 0 && (c->seqs <= 1 || ldq % 4 == 0);
   p.chunks = L.chunks;
   p.err = di->err;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(L.kernel.fn, dim3(L.ctas), kAttendThreads, L.smem, st, p);
+  cudaError_t e = launch_pdl(L.kernel.fn, dim3(L.ctas), kAttendThreads, L.kernel.smem, st, p);
   if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend");
   const int64_t rows = c->seqs * q_heads;
   const int wpr = rows <= int64_t(di->sms) * kJoinWarps ? kJoinWarps : 1;

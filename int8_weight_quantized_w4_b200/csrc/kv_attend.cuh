@@ -10,14 +10,21 @@
 // freely and each is read once.
 //
 // Work. The slots of one (sequence, key-value head, chunk of query heads), an
-// item, are cut into units of 64. All units of all items, in that order, are
+// item, are cut into units of 16 to 64, a tile for each warp. All units of all items, in that order, are
 // dealt to the CTAs in equal contiguous runs, by the lengths on the device: a
 // batch of unequal lengths, one long sequence and many short ones all load
-// every SM alike, and a CUDA graph stays valid while the lengths grow. A CTA
-// holds at most one item that began before its run and one that goes on
+// every SM alike, and a CUDA graph stays valid while the lengths grow. An item
+// counts kOver units more than it has, what beginning and ending it costs. A
+// CTA holds at most one item that began before its run and one that goes on
 // behind it; those leave (m, l, a) in the workspace and join_kernel joins them
 // in the order of the slots. So no result depends on timing, and nothing has
 // to be zero beforehand.
+//
+// Latency. Each warp feeds itself: its tiles of 4 to 16 slots follow one another
+// across the segments of its CTA's run, and while it works on one the next
+// ones are on their way into its ring of stages in shared memory (cp.async,
+// which also writes the zeros of slots that are not there), whichever segments
+// they belong to; their entries of the page table were fetched a tile earlier.
 #pragma once
 
 #include "kv_cache.cuh"
@@ -26,9 +33,10 @@ namespace w4kv {
 
 constexpr int kWarps = 4;
 constexpr int kAttendThreads = kWarps * 32;
-constexpr int kUnit = 64;  // slots of a unit: 4 warps x 16
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+constexpr int kOver = 1;  // an item's own cost, in units
 
 struct AttendParams {
   View c;
@@ -43,6 +51,8 @@ struct AttendParams {
   int64_t window;  // 0: every slot
   float scale2;    // scale * log2 e
   int32_t group, rows, chunks;  // query heads of a key-value head, of an item, items of a key-value head
+  int32_t unit_log;             // slots of a unit: a tile for each warp
+  int32_t q_vec;                // the rows of q are 16-byte aligned
   ErrorWord* err;
 };
 
@@ -52,236 +62,439 @@ __device__ __forceinline__ void attended(const AttendParams& p, int32_t b, int32
   lo = p.window > 0 && p.window < n ? n - static_cast<int32_t>(p.window) : 0;
 }
 
-__device__ __forceinline__ int32_t units_of(const AttendParams& p, int32_t b) {
+__device__ __forceinline__ int32_t units_of(const AttendParams& p, int32_t slots) {
+  return (slots + (1 << p.unit_log) - 1) >> p.unit_log;
+}
+
+// What an item of sequence b counts.
+__device__ __forceinline__ int32_t cost_of(const AttendParams& p, int32_t b) {
   int32_t lo, n;
   attended(p, b, lo, n);
-  return (n - lo + kUnit - 1) / kUnit;
+  return n > lo ? units_of(p, n - lo) + kOver : 0;
 }
 
-// The CTA that holds unit u, when `total` units are dealt to `ctas` of them:
-// the first total % ctas take one more than the others.
-__device__ __forceinline__ int64_t owner_of(int64_t u, int64_t total, int64_t ctas) {
-  const int64_t q = total / ctas, r = total % ctas;
-  return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q;
-}
-
-// Where this CTA's run of units begins, and its end.
+// How the units are dealt (shared by the CTA): each CTA takes `share` of them,
+// the first `extra` one more; this CTA's run ends before unit `end`. The host
+// keeps all units below 2^31.
 struct Run {
-  int64_t total, ctas, u, end;  // all units, CTAs that have any, this one's
-  int32_t b, item, unit;        // sequence, item within it, unit within that
+  int32_t share, extra, end;
+
+  // The CTA that holds unit u.
+  __device__ __forceinline__ int32_t owner(int32_t u) const {
+    const int32_t more = extra * (share + 1);
+    return u < more ? u / (share + 1) : extra + (u - more) / share;
+  }
 };
 
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
+// What is left of this CTA's run, in units that count kOver more an item.
+struct Walk {
+  int32_t left;
+  int32_t b, item, unit;  // sequence, item within it, unit within that
+  int32_t lo, n;          // attended slots of sequence b; n < 0: not read yet
+};
 
-// Every thread of the CTA calls it; `s` is shared scratch of kWarps + 3 words.
-__device__ inline bool find_run(const AttendParams& p, Run& r, int64_t* s) {
+// The slots [s0, s1) of one item.
+struct Segment {
+  int32_t b, h, q0, ng;               // sequence, key-value head, first query head and how many
+  int32_t s0, s1;
+  int32_t item, count;                // count: CTAs that the item takes, where it begins here; else 0
+  bool whole;
+};
+
+// Where this CTA's run begins; false if it has none. Every thread of the CTA
+// calls it; `s` is shared scratch.
+__device__ inline bool find_run(const AttendParams& p, Walk& w, Run& run, int32_t (&s)[kWarps + 3]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t items = int64_t(p.c.heads) * p.chunks;
-  int64_t mine = 0;
-  for (int32_t b = tid; b < p.c.seqs; b += kAttendThreads) mine += units_of(p, b);
-  mine = warp_sum(mine);
-  if (lane == 0) s[warp] = mine;
-  __syncthreads();
-  int64_t sum = 0;
+  const int32_t items = p.c.heads * p.chunks;
+  int32_t sum = 0;  // of all sequences' costs, where one pass does not hold them
+  if (p.c.seqs > kAttendThreads) {
+    int32_t mine = 0;
+    for (int32_t b = tid; b < p.c.seqs; b += kAttendThreads) mine += cost_of(p, b);
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0) s[warp] = mine;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) sum += s[w];
-  r.total = sum * items;
-  r.ctas = r.total < gridDim.x ? r.total : gridDim.x;
-  const int64_t c = blockIdx.x;
-  if (c >= r.ctas) return false;
-  const int64_t q = r.total / r.ctas, rest = r.total % r.ctas;
-  r.u = c * q + (c < rest ? c : rest);
-  r.end = r.u + q + (c < rest ? 1 : 0);
-  // the sequence of unit u: its predecessors hold at most u / items units per item
-  const int64_t want = r.u / items;
-  int64_t before = 0;
-  bool found = false;
-  for (int32_t b0 = 0; b0 < p.c.seqs && !found; b0 += kAttendThreads) {
+    for (int i = 0; i < kWarps; ++i) sum += s[i];
+  }
+  int32_t before = 0, want = 0, u = 0;
+  for (int32_t b0 = 0; b0 < p.c.seqs; b0 += kAttendThreads) {
     const int32_t b = b0 + tid;
-    const int64_t n = b < p.c.seqs ? units_of(p, b) : 0;
-    int64_t up = n;
+    const int32_t n = b < p.c.seqs ? cost_of(p, b) : 0;
+    int32_t up = n;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, up, o);
+      const int32_t v = __shfl_up_sync(0xffffffffu, up, o);
       if (lane >= o) up += v;
     }
     __syncthreads();
     if (lane == 31) s[warp] = up;
     if (tid == 0) s[kWarps] = -1;
     __syncthreads();
-    int64_t all = before;
+    int32_t all = before;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) up += s[w];
-      all += s[w];
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) up += s[i];
+      all += s[i];
     }
     up += before;
+    if (b0 == 0) {
+      if (p.c.seqs <= kAttendThreads) sum = all;
+      const int32_t total = sum * items, ctas = min(total, static_cast<int32_t>(gridDim.x)), c = blockIdx.x;
+      if (c >= ctas) return false;
+      const int32_t share = total / ctas, extra = total - share * ctas;
+      u = c * share + min(c, extra);
+      w.left = share + (c < extra ? 1 : 0);
+      if (tid == 0) run = {share, extra, u + w.left};
+      want = u / items;
+    }
     if (up - n <= want && want < up) {
       s[kWarps] = b;
       s[kWarps + 1] = up - n;
       s[kWarps + 2] = n;
     }
     __syncthreads();
-    found = s[kWarps] >= 0;
+    if (s[kWarps] >= 0) {
+      const int32_t inside = u - s[kWarps + 1] * items, cost = s[kWarps + 2];
+      w.b = s[kWarps];
+      w.n = -1;
+      w.item = inside / cost;
+      w.unit = inside - w.item * cost;
+      return true;
+    }
     before = all;
   }
-  if (!found) return false;
-  r.b = static_cast<int32_t>(s[kWarps]);
-  const int64_t inside = r.u - s[kWarps + 1] * items, n = s[kWarps + 2];
-  r.item = static_cast<int32_t>(inside / n);
-  r.unit = static_cast<int32_t>(inside % n);
-  return true;
+  return false;
 }
 
-// One CTA's run, segment by segment. Body::run leaves each warp's triple of
-// the segment in shared memory (m, l [kWarps][ROWS], a [kWarps][ROWS][dim]);
-// the CTA joins the four and writes the result, or a partial.
-template <class Body, int ROWS>
-__device__ __forceinline__ void attend_runs(const AttendParams& p, float* smem) {
-  __shared__ int64_t scratch[kWarps + 3];
-  const int D = p.c.dim;
-  float* sm_a = smem;
-  float* sm_m = sm_a + kWarps * ROWS * D;
-  float* sm_l = sm_m + kWarps * ROWS;
-  float* sm_body = sm_l + kWarps * ROWS;
-  Run r;
-  if (!find_run(p, r, scratch)) return;
-  const int q_heads = p.c.heads * p.group;
-  bool first = true;
-  while (r.u < r.end && r.b < p.c.seqs) {
-    int32_t lo, n;
-    attended(p, r.b, lo, n);
-    const int32_t units = (n - lo + kUnit - 1) / kUnit;
-    if (units == 0) {
-      ++r.b;
+// The next segment of the run; false at its end.
+__device__ __forceinline__ bool next_segment(const AttendParams& p, const Run& run, Walk& w, Segment& s) {
+  const int32_t items = p.c.heads * p.chunks;
+  while (w.left > 0 && w.b < p.c.seqs) {
+    if (w.n < 0) attended(p, w.b, w.lo, w.n);  // a sequence's first item
+    if (w.n == w.lo) {
+      ++w.b;
+      w.n = -1;
       continue;
     }
-    const int32_t stop = static_cast<int32_t>(min(int64_t(units), r.unit + (r.end - r.u)));
-    const int32_t h = r.item / p.chunks, g0 = (r.item % p.chunks) * p.rows;
-    const int ng = min(p.rows, p.group - g0);
-    const int32_t q0 = h * p.group + g0;
-    const int32_t s0 = lo + r.unit * kUnit, s1 = min(int64_t(n), lo + int64_t(stop) * kUnit);
-    Body::run(p, r.b, h, q0, ng, s0, s1, sm_a, sm_m, sm_l, sm_body);
-    __syncthreads();
-    const bool whole = r.unit == 0 && stop == units;
-    const int64_t slot = 2 * int64_t(blockIdx.x) + (first ? 0 : 1);
-    float* part = p.part + slot * p.part_stride;
-    for (int i = threadIdx.x; i < ng * D; i += kAttendThreads) {
-      const int g = i / D, d = i - g * D;
-      float M = -INFINITY;
+    const int32_t units = units_of(p, w.n - w.lo), cost = units + kOver;
+    const int32_t stop = min(cost - w.unit, w.left) + w.unit;
+    const int32_t from = max(0, w.unit - kOver), to = max(0, stop - kOver);
+    const int32_t last = run.end - w.left + (cost - w.unit) - 1;  // the item's last unit
+    s.b = w.b;
+    s.item = w.item;
+    s.s0 = w.lo + (from << p.unit_log);
+    s.s1 = s.s0 + min(w.n - s.s0, (to - from) << p.unit_log);
+    w.left -= stop - w.unit;
+    w.unit = 0;
+    if (stop == cost && ++w.item == items) {
+      w.item = 0;
+      ++w.b;
+      w.n = -1;
+    }
+    if (from == to) continue;
+    s.h = p.chunks == 1 ? s.item : s.item / p.chunks;
+    const int32_t g0 = (s.item - s.h * p.chunks) * p.rows;
+    s.q0 = s.h * p.group + g0;
+    s.ng = min(p.rows, p.group - g0);
+    s.whole = from == 0 && to == units;
+    s.count = 0;
+    if (from == 0) s.count = s.whole ? 1 : run.owner(last) - static_cast<int32_t>(blockIdx.x) + 1;
+    return true;
+  }
+  return false;
+}
+
+// A warp's tiles, ahead of the work on them.
+template <int TS>
+struct Ahead {
+  Walk w;
+  int32_t b, h, tile, s1;
+  bool live;
+
+  __device__ __forceinline__ void open(const AttendParams& p, const Run& run) {
+    Segment s;
+    do {
+      live = next_segment(p, run, w, s);
+      if (!live) return;
+      b = s.b;
+      h = s.h;
+      s1 = s.s1;
+      tile = s.s0 + static_cast<int32_t>(threadIdx.x >> 5) * TS;
+    } while (tile >= s1);
+  }
+  __device__ __forceinline__ void step(const AttendParams& p, const Run& run) {
+    if (!live) return;
+    tile += kWarps * TS;
+    if (tile >= s1) open(p, run);
+  }
+};
+
+// Queries of a segment on their way to shared memory: rows of WIDTH floats,
+// zeros behind head_dim and the last row.
+template <int ROWS, int WIDTH>
+struct Queries {
+  static constexpr int N = (ROWS * WIDTH / 4 + kAttendThreads - 1) / kAttendThreads;
+  float4 x[N];
+
+  __device__ __forceinline__ void fetch(const AttendParams& p, const Segment& s) {
+    const int D = p.c.dim;
+    const float* q = p.q + s.b * p.ldq + int64_t(s.q0) * D;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * ROWS + g]);
-      float l = 0.f, a = 0.f;
+    for (int n = 0; n < N; ++n) {
+      const int i = threadIdx.x + n * kAttendThreads, g = i / (WIDTH / 4), d = i % (WIDTH / 4) * 4;
+      x[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (g < s.ng && d < D) {
+        const float* from = q + g * D + d;
+        x[n] = p.q_vec ? *reinterpret_cast<const float4*>(from) : make_float4(from[0], from[1], from[2], from[3]);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(float* sq) const {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float m = sm_m[w * ROWS + g];
-        const float f = m == -INFINITY ? 0.f : ex2(m - M);
-        // a warp without slots holds zeros; a NaN that it holds stays one
-        l += m == -INFINITY ? sm_l[w * ROWS + g] : sm_l[w * ROWS + g] * f;
-        a += m == -INFINITY ? sm_a[(w * ROWS + g) * D + d] : sm_a[(w * ROWS + g) * D + d] * f;
+    for (int n = 0; n < N; ++n) {
+      const int i = threadIdx.x + n * kAttendThreads;
+      if (i < ROWS * WIDTH / 4) *reinterpret_cast<float4*>(sq + 4 * i) = x[n];
+    }
+  }
+};
+
+// The four warps' triples of a segment (a [ROWS][dim], m [ROWS], l [ROWS], each
+// in a stage of the warp's ring) joined, and written: the result, or a partial.
+template <int ROWS>
+__device__ __forceinline__ void finish(const AttendParams& p, const Segment& s, bool first, float* const (&triple)[kWarps]) {
+  const int D = p.c.dim;
+  const int64_t slot = 2 * int64_t(blockIdx.x) + (first ? 0 : 1);
+  float* part = p.part + slot * p.part_stride;
+  const int quads = D / 4;
+  for (int i = threadIdx.x; i < s.ng * quads; i += kAttendThreads) {
+    const int g = i / quads, d = 4 * (i - g * quads);
+    float m[kWarps], M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      m[w] = triple[w][ROWS * D + g];
+      M = fmaxf(M, m[w]);
+    }
+    float l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = m[w] == -INFINITY ? 1.f : ex2(m[w] - M);  // a warp without a score holds zeros, or a NaN
+      const float4 x = *reinterpret_cast<const float4*>(triple[w] + g * D + d);
+      l = fmaf(triple[w][ROWS * D + ROWS + g], f, l);
+      a = make_float4(fmaf(x.x, f, a.x), fmaf(x.y, f, a.y), fmaf(x.z, f, a.z), fmaf(x.w, f, a.w));
+    }
+    if (s.whole) {
+      float* o = p.out + s.b * p.ldo + int64_t(s.q0 + g) * D + d;
+      const float by = l == 0.f ? 0.f : 1.f / l;  // no slot with a weight: a is 0 too
+      o[0] = a.x * by;
+      o[1] = a.y * by;
+      o[2] = a.z * by;
+      o[3] = a.w * by;
+      if (d == 0) {
+        const float z = l == 0.f ? -INFINITY : M + log2f(l);
+        const int64_t at = int64_t(s.b) * p.c.heads * p.group + s.q0 + g;
+        if (p.lse != nullptr) p.lse[at] = z * kLn2;
+        if (p.lse2 != nullptr) p.lse2[at] = z;
       }
-      if (whole) {
-        p.out[r.b * p.ldo + int64_t(q0 + g) * D + d] = l == 0.f ? 0.f : a / l;
-        if (d == 0) {
-          const float z = l == 0.f ? -INFINITY : M + log2f(l);
-          const int64_t at = int64_t(r.b) * q_heads + q0 + g;
-          if (p.lse != nullptr) p.lse[at] = z * kLn2;
-          if (p.lse2 != nullptr) p.lse2[at] = z;
-        }
-      } else {
-        part[g * D + d] = a;
-        if (d == 0) {
-          part[p.rows * D + g] = M;
-          part[p.rows * D + p.rows + g] = l;
-        }
+    } else {
+      *reinterpret_cast<float4*>(part + g * D + d) = a;
+      if (d == 0) {
+        part[p.rows * D + g] = M;
+        part[p.rows * D + p.rows + g] = l;
       }
     }
-    if (r.unit == 0 && threadIdx.x == 0) {
-      const int64_t last = owner_of(r.u + units - 1, r.total, r.ctas);
-      p.meta[int64_t(r.b) * p.c.heads * p.chunks + r.item] =
-          make_int2(static_cast<int32_t>(slot), whole ? 1 : static_cast<int32_t>(last - blockIdx.x + 1));
+  }
+  if (s.count > 0 && threadIdx.x == 0)
+    p.meta[int64_t(s.b) * p.c.heads * p.chunks + s.item] = make_int2(static_cast<int32_t>(slot), s.count);
+}
+
+// One CTA's run. Body::segment leaves each warp's triple of a segment in the
+// free stage of its ring, where it stays until that warp's next tile is begun.
+template <class Body, int ROWS>
+__device__ __forceinline__ void attend_runs(const AttendParams& p, uint8_t* smem) {
+  __shared__ int32_t scratch[kWarps + 3];
+  __shared__ Run run;
+  __shared__ float* triple[kWarps];
+  float* sq = reinterpret_cast<float*>(smem + kWarps * Body::Feed::kRing);
+  float* body = sq + ROWS * Body::kWidth;
+  Walk w;
+  if (!find_run(p, w, run, scratch)) return;
+  __syncthreads();
+  typename Body::Feed feed;
+  feed.begin(p, run, w, smem + (threadIdx.x >> 5) * Body::Feed::kRing);
+  Segment s = {}, prev = {};
+  for (int k = 0;; ++k) {
+    const bool more = next_segment(p, run, w, s);
+    Queries<ROWS, Body::kWidth> queries;
+    if (more) queries.fetch(p, s);
+    if (k > 0) {
+      __syncthreads();  // every warp has left the segment before
+      finish<ROWS>(p, prev, k == 1, triple);
     }
-    first = false;
-    r.u += stop - r.unit;
-    r.unit = 0;
-    if (stop == units && ++r.item == p.c.heads * p.chunks) {
-      r.item = 0;
-      ++r.b;
-    }
+    if (!more) break;
+    queries.store(sq);
     __syncthreads();
+    float* to = Body::segment(p, run, s, feed, sq, body);
+    if ((threadIdx.x & 31) == 0) triple[threadIdx.x >> 5] = to;
+    prev = s;
   }
 }
 
 // ---------------------------------------------------------------- plain lanes
 
-// Loads of one tile's rows: which are there, and where.
-struct Row {
-  int64_t vec;    // first 16-byte vector of the slot's row in k and in v; -1: none
-  float ks, vs;   // int8 scales
+// A row's entry in the page table on its way from memory: looked at a tile
+// later, when it has arrived.
+struct Entry {
+  int32_t page, inner;  // inner < 0: no row
 };
 
-template <int TYPE>
-__device__ __forceinline__ Row find_row(const AttendParams& p, int32_t b, int32_t h, int32_t slot, int32_t s1) {
-  Row r = {-1, 0.f, 0.f};
-  if (slot < s1) {
-    const int32_t page = page_of(p.c, b, slot / p.c.slots_per_page, p.err, w4dev::K_KV_ATTEND);
-    if (page >= 0) {
-      const int32_t inner = h * p.c.slots_per_page + slot % p.c.slots_per_page;
-      r.vec = (int64_t(page) * p.c.page_stride + int64_t(inner) * p.c.dim) / Elem<TYPE>::kPerVec;
-      if constexpr (TYPE == W4_KV_I8) {
-        const int64_t at = int64_t(page) * p.c.heads * p.c.slots_per_page + inner;
-        r.ks = p.c.ks[at];
-        r.vs = p.c.vs[at];
-      }
+// How a warp's tiles of TS slots come to shared memory. CL lanes copy a row's
+// 16-byte vectors, CV each; rows lie PITCH vectors apart. SWIZZLED: the vectors
+// of each 128 bytes change places by the row's number in its tile, so that the
+// matrix body's reads (4 neighbours of 2 neighbouring rows, or 2 neighbours of
+// every other row) meet 8 different places.
+template <int TYPE, int TS_, int CL, int CV, int PITCH, bool SWIZZLED, int STAGES, int TRIPLE>
+struct Ring {
+  static constexpr int TS = TS_;
+  static constexpr bool I8 = TYPE == W4_KV_I8;
+  static constexpr int kSide = TS * PITCH * 16;  // bytes of a tile's keys, or values
+  static constexpr int kScales = 2 * kSide;      // then its int8 scales: keys' [TS], values' [TS]
+  static constexpr int kNeed = kScales + (I8 ? 8 * TS : 0);
+  static constexpr int kStage = ((kNeed > TRIPLE * 4 ? kNeed : TRIPLE * 4) + 127) / 128 * 128;
+  static constexpr int kRing = STAGES * kStage;
+  static constexpr int kRows = 32 / CL;          // rows of a copy instruction
+
+  Ahead<TS> ahead;
+  Entry entry;              // of the tile to be copied next
+  uint32_t held[STAGES];    // slots that are there, by lane: this tile's, the next one's ...
+  uint8_t* ring;
+  int put;                  // stage that is free: the next tile's
+
+  // Where vector `vec` of row `row` lies in a side of a stage.
+  __device__ static __forceinline__ int place(int row, int vec) {
+    if constexpr (SWIZZLED) vec ^= (((row >> 1) ^ (row << 1)) & 3) << 1;
+    return (row * PITCH + vec) * 16;
+  }
+
+  __device__ __forceinline__ void fetch_entry(const AttendParams& p) {
+    const int32_t lane = threadIdx.x & 31, slot = ahead.tile + lane;
+    entry = {0, -1};
+    if (ahead.live && lane < TS && slot < ahead.s1) {
+      const int32_t index = p.c.page.quotient(slot);
+      entry.inner = ahead.h * p.c.slots_per_page + (slot - index * p.c.slots_per_page);
+      entry.page = p.c.table[ahead.b * p.c.ldp + index];
     }
   }
-  return r;
-}
 
-// LPR lanes read a row, VPL 16-byte vectors each (interleaved, so that a load
-// instruction covers LPR * 16 contiguous bytes of it); a warp's tile is
-// 32 / LPR rows at a time, NP times. A lane keeps its part of every row's
-// product with q, so the sum over a row's lanes leaves the score with each
-// of them and the same lanes add the row's values without an exchange; each
-// group of LPR lanes carries its own (m, l, a) and the groups join at the end.
+  // The copies of the next tile into the free stage, as one group.
+  __device__ __forceinline__ void push(const AttendParams& p, const Run& run) {
+    const int lane = threadIdx.x & 31;
+    uint8_t* stage = ring + put * kStage;
+    put = put + 1 == STAGES ? 0 : put + 1;
+    bool there = entry.inner >= 0;
+    if (there && (entry.page < 0 || entry.page >= p.c.num_pages)) {
+      w4dev::record_error(p.err, W4_ERR_VALUE, w4dev::K_KV_ATTEND, entry.page);
+      there = false;
+    }
+    const uint32_t mask = __ballot_sync(0xffffffffu, there);
+#pragma unroll
+    for (int i = 0; i + 1 < STAGES; ++i) held[i] = held[i + 1];
+    held[STAGES - 1] = mask;
+    if (ahead.live) {
+      const uint32_t at = there ? static_cast<uint32_t>(entry.page) * p.c.page_rows + entry.inner : 0u;
+      const uint32_t n16 = p.c.dim / Elem<TYPE>::kPerVec;
+      const int vec = lane % CL;
+#pragma unroll
+      for (int i = 0; i < TS / kRows; ++i) {
+        const int row = i * kRows + lane / CL;
+        const uint64_t from = uint64_t(__shfl_sync(0xffffffffu, at, row)) * (n16 * 16) + vec * 16;
+        const uint8_t* k = static_cast<const uint8_t*>(p.c.k) + from;
+        const uint8_t* v = static_cast<const uint8_t*>(p.c.v) + from;
+        const bool copy = (mask >> row) & 1u;
+#pragma unroll
+        for (int j = 0; j < CV; ++j) {
+          const bool in = copy && vec + j * CL < n16;  // else zeros are written, and nothing read
+          const int to = place(row, vec + j * CL);
+          w4dev::cp_async_16(stage + to, in ? k + j * CL * 16 : p.c.k, in ? 16 : 0);
+          w4dev::cp_async_16(stage + kSide + to, in ? v + j * CL * 16 : p.c.v, in ? 16 : 0);
+        }
+      }
+      if constexpr (I8) {
+        // lanes 0..TS-1 hold the rows; scales of keys, then of values
+        const int64_t scale = int64_t(entry.page) * (p.c.heads * p.c.slots_per_page) + entry.inner;
+        if (lane < TS) {
+          float* to = reinterpret_cast<float*>(stage + kScales);
+          copy4(to + lane, there ? p.c.ks + scale : p.c.ks, there);
+          copy4(to + TS + lane, there ? p.c.vs + scale : p.c.vs, there);
+        }
+      }
+    }
+    w4dev::cp_async_commit();
+    ahead.step(p, run);
+    fetch_entry(p);
+  }
+
+  __device__ static __forceinline__ void copy4(float* dst, const float* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(w4dev::smem_u32(dst)), "l"(src), "r"(there ? 4 : 0)
+                 : "memory");
+  }
+
+  __device__ __forceinline__ void begin(const AttendParams& p, const Run& run, const Walk& w, uint8_t* own) {
+    ring = own;
+    put = 0;
+    ahead.w = w;
+    ahead.open(p, run);
+    fetch_entry(p);
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) held[i] = 0;
+#pragma unroll
+    for (int i = 0; i + 1 < STAGES; ++i) push(p, run);
+  }
+
+  // The next tile, arrived: its stage and its slots' mask; the one behind the
+  // stages ahead is begun. The tile before is given up.
+  __device__ __forceinline__ const uint8_t* take(const AttendParams& p, const Run& run, uint32_t& mask) {
+    w4dev::cp_async_wait_group<STAGES - 2>();
+    __syncwarp();
+    const int at = put + 1 == STAGES ? 0 : put + 1;
+    push(p, run);
+    mask = held[0];
+    return ring + at * kStage;
+  }
+
+  // The stage that no tile is in: free until the next take().
+  __device__ __forceinline__ float* spare() const {
+    __syncwarp();  // the last tile may lie there
+    return reinterpret_cast<float*>(ring + put * kStage);
+  }
+};
+
+// LPR lanes read a row, VPL 16-byte vectors each; a warp reads 32 / LPR rows at
+// a time. A lane keeps its part of every row's product with q, so the sum over
+// a row's lanes leaves the score with each of them and the same lanes add the
+// row's values without an exchange; each group of LPR lanes carries its own
+// (m, l, a) and the groups join at the end. Tiles are 4 KB (K and V) or a
+// little less, whatever the rows: 16, 8 or 4 slots.
 template <int TYPE, int LPR, int VPL, int GT>
 struct PlainLanes {
   using E = Elem<TYPE>;
   static constexpr int EPV = E::kPerVec;
   static constexpr int RPW = 32 / LPR;
-  static constexpr int NP = LPR == 4 ? 2 : (VPL * GT >= 8 || VPL > 4 ? 2 : 4);
+  static constexpr int kRowBytes = LPR * VPL * 16;
+  static constexpr int NP = kRowBytes * 16 <= 2048 && RPW < 16 ? 16 / RPW : (kRowBytes * 8 <= 2048 && RPW <= 8 ? 8 / RPW : 1);
   static constexpr int TS = NP * RPW;
-  static constexpr int kBodyFloats = GT * LPR * VPL * EPV;
+  static constexpr int kWidth = LPR * VPL * EPV;  // of a row of queries in shared memory
+  static constexpr int kBodyFloats = 0;
+  static constexpr int kMinCtas = GT * VPL * EPV <= 16 ? 5 : (GT * VPL * EPV <= 32 ? 4 : (GT * VPL * EPV <= 64 ? 3 : 2));
+  using Feed = Ring<TYPE, TS, LPR, VPL, LPR * VPL, false, 2, GT * (kWidth + 2)>;
 
-  __device__ static __forceinline__ void load(uint4 (&x)[NP][VPL], const void* base, const Row& row, int n16) {
-    const int lane = threadIdx.x & 31, sub = lane % LPR, rg = lane / LPR;
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int64_t at = __shfl_sync(0xffffffffu, row.vec, i * RPW + rg);
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        const int vec = sub + j * LPR;
-        x[i][j] = make_uint4(0, 0, 0, 0);
-        if (at >= 0 && vec < n16) x[i][j] = __ldg(static_cast<const uint4*>(base) + at + vec);
-      }
-    }
-  }
-
-  __device__ static __forceinline__ void run(const AttendParams& p, int32_t b, int32_t h, int32_t q0, int ng,
-                                             int32_t s0, int32_t s1, float* sm_a, float* sm_m, float* sm_l,
-                                             float* sq) {
+  // The warp's triple of the segment, and where it has been put.
+  __device__ static __forceinline__ float* segment(const AttendParams& p, const Run& run, const Segment& seg, Feed& feed,
+                                                   const float* sq, float*) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR, rg = lane / LPR;
     const int D = p.c.dim, n16 = D / EPV;
-    constexpr int W = LPR * VPL * EPV;
-    for (int i = threadIdx.x; i < GT * W; i += kAttendThreads) {
-      const int g = i / W, d = i % W;
-      sq[i] = g < ng && d < D ? p.q[b * p.ldq + int64_t(q0 + g) * D + d] : 0.f;
-    }
-    __syncthreads();
+    constexpr int W = kWidth;
+    const int32_t s1 = seg.s1;
     float m[GT], l[GT], a[GT][VPL * EPV];
 #pragma unroll
     for (int g = 0; g < GT; ++g) {
@@ -290,15 +503,12 @@ struct PlainLanes {
 #pragma unroll
       for (int d = 0; d < VPL * EPV; ++d) a[g][d] = 0.f;
     }
-    uint4 kx[NP][VPL], vx[NP][VPL];
-    int32_t t = s0 + warp * TS;
-    Row row = find_row<TYPE>(p, b, h, t + lane, min(s1, t + TS));
-    load(kx, p.c.k, row, n16);
-    load(vx, p.c.v, row, n16);
 #pragma unroll 1
-    while (t < s1) {
-      const int32_t next = t + kWarps * TS;
-      const Row next_row = find_row<TYPE>(p, b, h, next + lane, min(s1, next + TS));
+    for (int32_t t = seg.s0 + warp * TS; t < s1; t += kWarps * TS) {
+      uint32_t held;
+      const uint8_t* stage = feed.take(p, run, held);
+      const uint8_t* mine = stage + Feed::place(rg, sub);
+      const float* scales = reinterpret_cast<const float*>(stage + Feed::kScales);
       float x[GT][NP];
 #pragma unroll
       for (int g = 0; g < GT; ++g)
@@ -316,29 +526,24 @@ struct PlainLanes {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           float f[EPV];
-          E::unpack(kx[i][j], f);
+          E::unpack(*reinterpret_cast<const uint4*>(mine + i * RPW * kRowBytes + j * LPR * 16), f);
 #pragma unroll
           for (int g = 0; g < GT; ++g)
 #pragma unroll
             for (int e = 0; e < EPV; ++e) x[g][i] = fmaf(qv[g][e], f[e], x[g][i]);
         }
       }
-      load(kx, p.c.k, next_row, n16);
 #pragma unroll
       for (int g = 0; g < GT; ++g)
 #pragma unroll
         for (int i = 0; i < NP; ++i)
 #pragma unroll
           for (int o = 1; o < LPR; o *= 2) x[g][i] += __shfl_xor_sync(0xffffffffu, x[g][i], o);
-      float vs[NP];
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const bool there = __shfl_sync(0xffffffffu, row.vec, i * RPW + rg) >= 0;
+        const bool there = (held >> (i * RPW + rg)) & 1u;
         float f = p.scale2;
-        if constexpr (TYPE == W4_KV_I8) {
-          f *= __shfl_sync(0xffffffffu, row.ks, i * RPW + rg);
-          vs[i] = __shfl_sync(0xffffffffu, row.vs, i * RPW + rg);
-        }
+        if constexpr (TYPE == W4_KV_I8) f *= scales[i * RPW + rg];
 #pragma unroll
         for (int g = 0; g < GT; ++g) x[g][i] = there ? x[g][i] * f : -INFINITY;
       }
@@ -348,8 +553,8 @@ struct PlainLanes {
           const int32_t slot = t + i * RPW + rg;
 #pragma unroll
           for (int g = 0; g < GT; ++g)
-            if (sub == g % LPR && g < ng && slot < s1)
-              p.scores[(int64_t(b) * p.c.heads * p.group + q0 + g) * p.c.capacity + slot] = x[g][i];
+            if (sub == g % LPR && g < seg.ng && slot < s1)
+              p.scores[(int64_t(seg.b) * p.c.heads * p.group + seg.q0 + g) * p.c.capacity + slot] = x[g][i];
         }
       }
 #pragma unroll
@@ -358,8 +563,8 @@ struct PlainLanes {
 #pragma unroll
         for (int i = 0; i < NP; ++i) top = fmaxf(top, x[g][i]);
         if (top > m[g]) {
-          const float f = m[g] == -INFINITY ? 0.f : ex2(m[g] - top);
           if (m[g] != -INFINITY) {
+            const float f = ex2(m[g] - top);
             l[g] *= f;
 #pragma unroll
             for (int d = 0; d < VPL * EPV; ++d) a[g][d] *= f;
@@ -371,7 +576,7 @@ struct PlainLanes {
         for (int i = 0; i < NP; ++i) {
           x[g][i] = ex2(x[g][i] - ref);
           l[g] += x[g][i];
-          if constexpr (TYPE == W4_KV_I8) x[g][i] = x[g][i] * vs[i];
+          if constexpr (TYPE == W4_KV_I8) x[g][i] *= scales[TS + i * RPW + rg];
         }
       }
 #pragma unroll
@@ -379,17 +584,15 @@ struct PlainLanes {
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
           float f[EPV];
-          E::unpack(vx[i][j], f);
+          E::unpack(*reinterpret_cast<const uint4*>(mine + Feed::kSide + i * RPW * kRowBytes + j * LPR * 16), f);
 #pragma unroll
           for (int g = 0; g < GT; ++g)
 #pragma unroll
             for (int e = 0; e < EPV; ++e) a[g][j * EPV + e] = fmaf(x[g][i], f[e], a[g][j * EPV + e]);
         }
-      load(vx, p.c.v, next_row, n16);
-      row = next_row;
-      t = next;
     }
     // the groups' triples into one
+    float* to = feed.spare();
 #pragma unroll
     for (int g = 0; g < GT; ++g) {
       float top = m[g];
@@ -406,8 +609,8 @@ struct PlainLanes {
         for (int o = LPR; o < 32; o *= 2) a[g][d] += __shfl_xor_sync(0xffffffffu, a[g][d], o);
       }
       if (lane == 0) {
-        sm_m[warp * GT + g] = top;
-        sm_l[warp * GT + g] = l[g];
+        to[GT * D + g] = top;
+        to[GT * D + GT + g] = l[g];
       }
       if (rg == 0) {
 #pragma unroll
@@ -415,17 +618,19 @@ struct PlainLanes {
           const int vec = sub + j * LPR;
           if (vec < n16) {
 #pragma unroll
-            for (int e = 0; e < EPV; ++e) sm_a[(warp * GT + g) * D + vec * EPV + e] = a[g][j * EPV + e];
+            for (int e = 0; e < EPV; e += 4)
+              *reinterpret_cast<float4*>(to + g * D + vec * EPV + e) = *reinterpret_cast<const float4*>(&a[g][j * EPV + e]);
           }
         }
       }
     }
+    return to;
   }
 };
 
 template <class Body, int ROWS>
-__global__ void __launch_bounds__(kAttendThreads) attend_kernel(const AttendParams p) {
-  extern __shared__ __align__(16) float attend_smem[];
+__global__ void __launch_bounds__(kAttendThreads, Body::kMinCtas) attend_kernel(const AttendParams p) {
+  extern __shared__ __align__(128) uint8_t attend_smem[];
   pdl_launch_dependents();
   pdl_wait();
   attend_runs<Body, ROWS>(p, attend_smem);
@@ -434,9 +639,16 @@ __global__ void __launch_bounds__(kAttendThreads) attend_kernel(const AttendPara
 // A kernel of the table: how it is launched, what it takes.
 struct AttendKernel {
   void (*fn)(const AttendParams);
-  int rows;        // query heads of an item
-  int body_floats; // shared memory of the body
+  int rows;         // query heads of an item
+  int unit;         // slots of a unit
+  size_t smem;      // bytes of shared memory
 };
+
+template <class Body, int ROWS>
+AttendKernel attend_kernel_of() {
+  return {attend_kernel<Body, ROWS>, ROWS, kWarps * Body::TS,
+          size_t(kWarps) * Body::Feed::kRing + (size_t(ROWS) * Body::kWidth + Body::kBodyFloats) * 4};
+}
 
 // The kernel for a call of this element type (one translation unit a type).
 template <int TYPE>
@@ -444,11 +656,9 @@ AttendKernel attend_kernel_for(int32_t dim, int32_t group);
 
 template <int TYPE, int LPR, int VPL>
 AttendKernel plain_kernel_for(int32_t group) {
-  if (group == 1)
-    return {attend_kernel<PlainLanes<TYPE, LPR, VPL, 1>, 1>, 1, PlainLanes<TYPE, LPR, VPL, 1>::kBodyFloats};
-  if (group == 2)
-    return {attend_kernel<PlainLanes<TYPE, LPR, VPL, 2>, 2>, 2, PlainLanes<TYPE, LPR, VPL, 2>::kBodyFloats};
-  return {attend_kernel<PlainLanes<TYPE, LPR, VPL, 4>, 4>, 4, PlainLanes<TYPE, LPR, VPL, 4>::kBodyFloats};
+  if (group == 1) return attend_kernel_of<PlainLanes<TYPE, LPR, VPL, 1>, 1>();
+  if (group == 2) return attend_kernel_of<PlainLanes<TYPE, LPR, VPL, 2>, 2>();
+  return attend_kernel_of<PlainLanes<TYPE, LPR, VPL, 4>, 4>();
 }
 
 // The narrowest shape that holds a row's vectors.

@@ -1,10 +1,12 @@
 // The attention kernels over a cache of W4_KV_BF16 elements.
-#include "kv_attend.cuh"
+#include "kv_attend_mma.cuh"
 
 namespace w4kv {
 
 template <>
 AttendKernel attend_kernel_for<W4_KV_BF16>(int32_t dim, int32_t group) {
+  if (group >= 3 && dim <= 128)
+    return group <= 4 ? matrix_kernel_for<W4_KV_BF16, 4>(dim) : matrix_kernel_for<W4_KV_BF16, 8>(dim);
   return plain_kernel_for<W4_KV_BF16>(dim, group);
 }
 

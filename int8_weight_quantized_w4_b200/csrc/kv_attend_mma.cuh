@@ -1,0 +1,364 @@
+// The matrix-instruction body of kv_attend, for several query heads on one
+// key-value head: at 4 heads and more the plain lanes' fused multiply-adds
+// (one for each head and stored element) take longer than the loads.
+//
+// Exactness. A stored key or value is an exact fp16 (fp16, int8 codes) or
+// bf16 operand; the fp32 queries and softmax weights are taken apart into
+// pieces of that type, which lie in different rows of the 16-row A operand
+// and are added up in fp32 behind the product:
+//   fp16, int8: 8 heads x 2 pieces, 11 + 11 bits: the second one holds the
+//               exact rest, scaled by 2^11. Queries and weights are scaled by
+//               powers of two so that their largest lies at 2^14: what is left
+//               out is below 2^-22 of each of them or 2^-50 of the largest;
+//   bf16:       4 heads x 3 pieces (8 + 8 + 8 bits, all of them) in one
+//               instruction, or 8 heads in two (pieces 0 and 1, then 2).
+//
+// Layout. mma.m16n8k16 sums over k in any order, and its n columns may be any
+// 8 values, so both operands are read from the stages as they were stored, 16
+// bytes a lane, without a transposing load: lane (g, t) = (lane / 4, lane % 4) reads
+//   keys:   vectors t, t + 4, ... of slots g and g + 8 of a tile's 16; the 8
+//           elements of a vector are two k-steps' 4 each;
+//   values: vectors g, g + 8 of slots 2t, 2t+1, 2t+8, 2t+9; byte permutes pair
+//           the slots, element j of all vectors makes one product's columns.
+// The scores' accumulators are then the A operand of the second product.
+#pragma once
+
+#include "kv_attend.cuh"
+
+namespace w4kv {
+
+template <int TYPE>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint4 a, uint32_t b0, uint32_t b1) {
+  if constexpr (TYPE == W4_KV_BF16) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+  } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+  }
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+
+// Two bytes (code XOR 0x80) under the high byte of fp16 1024 are 1024 + 128 +
+// code; the subtraction is exact.
+__device__ __forceinline__ uint32_t code_pair(uint32_t biased, uint32_t sel) {
+  const uint32_t w = prmt(biased, 0x64646464u, sel);
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&w), __floats2half2_rn(1152.f, 1152.f));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Piece `piece` of x (two neighbours packed): fp16's second one is scaled by 2^11.
+__device__ __forceinline__ uint32_t half_piece(float a, float b, int piece) {
+  if (piece == 0) return pack_half(a, b);
+  return pack_half((a - __half2float(__float2half_rn(a))) * 2048.f, (b - __half2float(__float2half_rn(b))) * 2048.f);
+}
+
+__device__ __forceinline__ float bf16_rest(float x) { return x - __bfloat162float(__float2bfloat16_rn(x)); }
+
+__device__ __forceinline__ uint32_t bf16_piece(float a, float b, int piece) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i < piece) {
+      a = bf16_rest(a);
+      b = bf16_rest(b);
+    }
+  }
+  return pack_bf16(a, b);
+}
+
+__device__ __forceinline__ float power_of_two(int exponent) {  // exponent in -126..127
+  return __uint_as_float(static_cast<uint32_t>(exponent + 127) << 23);
+}
+
+// ROWS query heads, rows of at most MAXD elements.
+template <int TYPE, int ROWS, int MAXD>
+struct MatrixLanes {
+  using E = Elem<TYPE>;
+  static constexpr bool BF = TYPE == W4_KV_BF16, I8 = TYPE == W4_KV_I8;
+  static_assert(BF || ROWS == 8, "fp16 pieces of 8 heads fill the 16 rows");
+  static constexpr int SETS = BF && ROWS == 8 ? 2 : 1;  // A operands
+  static constexpr int EPV = E::kPerVec;
+  static constexpr int NI = (MAXD / EPV + 3) / 4;       // key vectors of a lane
+  static constexpr int STEPS = NI * EPV / 4;            // k-steps of the scores
+  static constexpr int VB = I8 && MAXD <= 64 ? 8 : 16;  // bytes of a value load
+  static constexpr int VE = VB / E::kBytes;             // its elements
+  static constexpr int NC = (MAXD / VE + 7) / 8;        // value vectors of a lane
+  static constexpr int NT = 1;                          // tiles of 16 slots at once
+  static constexpr int TS = 16 * NT;
+  static constexpr int kLift = BF ? 0 : 14;  // fp16 pieces: the exponent of the largest value
+  static constexpr int kFrag = SETS * STEPS * 32 * 4;   // words of the queries' operands
+  static constexpr int kWidth = MAXD;  // of a row of queries in shared memory
+  static constexpr int kBodyFloats = kFrag;
+  static constexpr int kMinCtas = 3;
+  static constexpr int CV = MAXD == 96 ? 3 : 1;         // copies: lanes of a row, vectors of a lane
+  static constexpr int CL = MAXD / EPV / CV;
+  using Feed = Ring<TYPE, TS, CL, CV, (MAXD / EPV + 7) / 8 * 8, true, 2, ROWS * (MAXD + 2)>;
+  using VVec = typename std::conditional<VB == 16, uint4, uint2>::type;
+
+  __device__ static __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+  __device__ static __forceinline__ uint32_t word(const uint2& v, int i) { return i == 0 ? v.x : v.y; }
+
+  // The queries as A operands in shared memory, in the order the lanes read
+  // them; returns what this lane's head's scores are multiplied by for it.
+  __device__ static __forceinline__ float stage_queries(uint32_t* frag, const float* sq) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    float factor = 1.f, scale = 1.f;
+    if constexpr (!BF) {
+      // 2^(14 - e), 2^e the power below the largest |q| of each row; the scores take it back
+#pragma unroll
+      for (int h = 0; h < ROWS; ++h) {
+        uint32_t top = 0;
+        if (4 * lane < MAXD) {
+          const float4 x = *reinterpret_cast<const float4*>(sq + h * MAXD + 4 * lane);
+          top = max(max(__float_as_uint(fabsf(x.x)), __float_as_uint(fabsf(x.y))),
+                    max(__float_as_uint(fabsf(x.z)), __float_as_uint(fabsf(x.w))));
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (h == g) factor = power_of_two(max(kLift + 1, min(253, static_cast<int>(top >> 23))) - 127 - kLift);
+      }
+      scale = 1.f / factor;
+    }
+    for (int s = warp; s < SETS * STEPS; s += kWarps) {
+      const int set = s / STEPS, st = s % STEPS;
+      const int d = (t + 4 * (st / (EPV / 4))) * EPV + 4 * (st % (EPV / 4));
+      uint32_t a[4];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r = g + 8 * half;
+        const int h = r % ROWS, piece = ROWS == 4 ? r / 4 : (set == 0 ? r / 8 : 2 + r / 8);
+        const float4 x = *reinterpret_cast<const float4*>(sq + h * MAXD + d);  // zeros behind head_dim
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float u = (e == 0 ? x.x : x.z) * scale, v = (e == 0 ? x.y : x.w) * scale;
+          if constexpr (BF) {
+            a[half + 2 * e] = piece < 3 ? bf16_piece(u, v, piece) : 0u;
+          } else {
+            a[half + 2 * e] = half_piece(u, v, piece);
+          }
+        }
+      }
+      *reinterpret_cast<uint4*>(frag + (s * 32 + lane) * 4) = make_uint4(a[0], a[1], a[2], a[3]);
+    }
+    __syncthreads();
+    return factor;
+  }
+
+  // Rows of one head's pieces summed: in a lane, and over the two lanes that
+  // share a head where there are 4.
+  __device__ static __forceinline__ float joined(float lo, float hi) {
+    if constexpr (!BF) return fmaf(hi, 1.f / 2048.f, lo);
+    float v = lo + hi;
+    if constexpr (ROWS == 4) v += __shfl_xor_sync(0xffffffffu, v, 16);
+    return v;
+  }
+
+  // The warp's triple of the segment, and where it has been put.
+  __device__ static __forceinline__ float* segment(const AttendParams& p, const Run& run, const Segment& seg, Feed& feed,
+                                                   const float* sq, float* body) {
+    uint32_t* frag = reinterpret_cast<uint32_t*>(body);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int D = p.c.dim, head = g % ROWS;
+    const int32_t s1 = seg.s1;
+    const float scale = stage_queries(frag, sq) * p.scale2;
+    float m = -INFINITY, l = 0.f;
+    float acc[NC * VE][4];
+#pragma unroll
+    for (int i = 0; i < NC * VE; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    int vexp = 1;  // int8: exponent field of the largest value scale so far; acc is in units of 2^(vexp - 127)
+#pragma unroll 1
+    for (int32_t tile = seg.s0 + warp * TS; tile < s1; tile += kWarps * TS) {
+      uint32_t held;
+      const uint8_t* stage = feed.take(p, run, held);
+      const float* scales = reinterpret_cast<const float*>(stage + Feed::kScales);
+      uint4 kx[2 * NT][NI];
+#pragma unroll
+      for (int n = 0; n < 2 * NT; ++n)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) kx[n][i] = *reinterpret_cast<const uint4*>(stage + Feed::place(8 * n + g, t + 4 * i));
+      float c[2 * NT][4] = {}, odd[2 * NT][4] = {};  // int8 has the registers for two chains of products
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st) {
+        const int i = st / (EPV / 4), j = st % (EPV / 4);
+        uint4 a[SETS];
+#pragma unroll
+        for (int s = 0; s < SETS; ++s) a[s] = *reinterpret_cast<const uint4*>(frag + ((s * STEPS + st) * 32 + lane) * 4);
+#pragma unroll
+        for (int n = 0; n < 2 * NT; ++n) {
+          uint32_t b0, b1;
+          if constexpr (I8) {
+            const uint32_t w = word(kx[n][i], j) ^ 0x80808080u;
+            b0 = code_pair(w, 0x4140);
+            b1 = code_pair(w, 0x4342);
+          } else {
+            b0 = word(kx[n][i], 2 * j);
+            b1 = word(kx[n][i], 2 * j + 1);
+          }
+#pragma unroll
+          for (int s = 0; s < SETS; ++s) mma16816<TYPE>(I8 && (st & 1) ? odd[n] : c[n], a[s], b0, b1);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 2 * NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if constexpr (I8) c[n][e] += odd[n][e];
+      VVec vx[4 * NT][NC];
+#pragma unroll
+      for (int n = 0; n < 4 * NT; ++n)
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) {
+          const int row = 2 * t + (n & 1) + (n >> 1) * 8, byte = (g + 8 * cc) * VB;
+          vx[n][cc] = *reinterpret_cast<const VVec*>(stage + Feed::kSide + Feed::place(row, byte / 16) + byte % 16);
+        }
+      // scores of this lane's head at slots 8 n + 2 t + e
+      float x[2 * NT][2];
+      float top = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < 2 * NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int slot = 8 * n + 2 * t + e;
+          float f = scale;
+          if constexpr (I8) f *= scales[slot];
+          const float v = joined(c[n][e], c[n][2 + e]) * f;
+          x[n][e] = (held >> slot) & 1u ? v : -INFINITY;
+          top = fmaxf(top, x[n][e]);
+        }
+      if (p.scores != nullptr && head < seg.ng && g < ROWS) {
+        float* to = p.scores + (int64_t(seg.b) * p.c.heads * p.group + seg.q0 + head) * p.c.capacity + tile + 2 * t;
+#pragma unroll
+        for (int n = 0; n < 2 * NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (tile + 8 * n + 2 * t + e < s1) to[8 * n + e] = x[n][e];
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // weights are 2^(x - m), the largest 2^kLift: the triple's m lies that far below its scores
+      top = fmaxf(m, top - kLift);
+      float back = m == -INFINITY ? 1.f : ex2(m - top);  // without a score so far there are zeros, or a NaN
+      l *= back;
+      m = top;
+      float unit = 1.f;
+      if constexpr (I8) {
+        const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(scales[TS + lane % TS]))) >> 23);
+        const int now = max(vexp, min(e, 253));
+        const int fall = vexp - now;
+        if (fall != 0) back = fall < -126 ? back * 0.f : back * power_of_two(fall);
+        vexp = now;
+        unit = power_of_two(127 - now);
+      }
+      if (__any_sync(0xffffffffu, back != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < NC * VE; ++i) {
+          acc[i][0] *= back;
+          acc[i][1] *= back;
+          acc[i][2] *= back;
+          acc[i][3] *= back;
+        }
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int n = 0; n < 2 * NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[n][e] = ex2(x[n][e] - ref);
+          l += x[n][e];
+          if constexpr (I8) x[n][e] *= scales[TS + 8 * n + 2 * t + e] * unit;
+        }
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        uint4 w[SETS];
+        const float(&x0)[2] = x[2 * k];
+        const float(&x1)[2] = x[2 * k + 1];
+        if constexpr (!BF) {
+          w[0] = make_uint4(half_piece(x0[0], x0[1], 0), half_piece(x0[0], x0[1], 1), half_piece(x1[0], x1[1], 0),
+                            half_piece(x1[0], x1[1], 1));
+        } else {
+          uint32_t piece[3][2];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            piece[i][0] = bf16_piece(x0[0], x0[1], i);
+            piece[i][1] = bf16_piece(x1[0], x1[1], i);
+          }
+          if constexpr (ROWS == 4) {
+            const bool low = g < 4;  // rows 0-3 and 8-11: pieces 0 and 2; rows 4-7: piece 1
+            w[0] = make_uint4(low ? piece[0][0] : piece[1][0], low ? piece[2][0] : 0u,
+                              low ? piece[0][1] : piece[1][1], low ? piece[2][1] : 0u);
+          } else {
+            w[0] = make_uint4(piece[0][0], piece[1][0], piece[0][1], piece[1][1]);
+            w[SETS - 1] = make_uint4(piece[2][0], 0u, piece[2][1], 0u);
+          }
+        }
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) {
+          if constexpr (I8) {
+#pragma unroll
+            for (int q = 0; q < VE / 4; ++q) {
+              uint32_t s[4];
+#pragma unroll
+              for (int n = 0; n < 4; ++n) s[n] = word(vx[4 * k + n][cc], q) ^ 0x80808080u;
+              const uint32_t lo0 = prmt(s[0], s[1], 0x5140), hi0 = prmt(s[0], s[1], 0x7362);
+              const uint32_t lo1 = prmt(s[2], s[3], 0x5140), hi1 = prmt(s[2], s[3], 0x7362);
+              mma16816<TYPE>(acc[cc * VE + 4 * q], w[0], code_pair(lo0, 0x4140), code_pair(lo1, 0x4140));
+              mma16816<TYPE>(acc[cc * VE + 4 * q + 1], w[0], code_pair(lo0, 0x4342), code_pair(lo1, 0x4342));
+              mma16816<TYPE>(acc[cc * VE + 4 * q + 2], w[0], code_pair(hi0, 0x4140), code_pair(hi1, 0x4140));
+              mma16816<TYPE>(acc[cc * VE + 4 * q + 3], w[0], code_pair(hi0, 0x4342), code_pair(hi1, 0x4342));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+              const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
+              const uint32_t b0 = prmt(word(vx[4 * k][cc], j / 2), word(vx[4 * k + 1][cc], j / 2), sel);
+              const uint32_t b1 = prmt(word(vx[4 * k + 2][cc], j / 2), word(vx[4 * k + 3][cc], j / 2), sel);
+#pragma unroll
+              for (int s = 0; s < SETS; ++s) mma16816<TYPE>(acc[cc * VE + j], w[s], b0, b1);
+            }
+          }
+        }
+      }
+    }
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    const float unit = I8 ? power_of_two(vexp - 127) : 1.f;
+    float* to = feed.spare();
+    if (t == 0 && g < ROWS) {
+      to[ROWS * D + head] = m;
+      to[ROWS * D + ROWS + head] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < NC * VE; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float v = joined(acc[i][e], acc[i][2 + e]) * unit;
+        const int d = (2 * t + e + 8 * (i / VE)) * VE + i % VE;
+        if (g < ROWS && d < D) to[head * D + d] = v;
+      }
+    return to;
+  }
+};
+
+// The matrix kernel for this many query heads, where there is one.
+template <int TYPE, int ROWS>
+AttendKernel matrix_kernel_for(int32_t dim) {
+  if (dim <= 64) return attend_kernel_of<MatrixLanes<TYPE, ROWS, 64>, ROWS>();
+  if constexpr (TYPE != W4_KV_I8) {
+    if (dim <= 96) return attend_kernel_of<MatrixLanes<TYPE, ROWS, 96>, ROWS>();
+  }
+  return attend_kernel_of<MatrixLanes<TYPE, ROWS, 128>, ROWS>();
+}
+
+}  // namespace w4kv

@@ -15,9 +15,20 @@ namespace w4kv {
 
 using w4dev::ErrorWord;
 
+// Quotients by a divisor of 1..2^30 of dividends below 2^31, by one high
+// product: with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d =
+// (floor(m n / 2^32) + n) >> l.
+struct Divisor {
+  uint32_t d, m, l;
+  __device__ __forceinline__ int32_t quotient(int32_t n) const {
+    return static_cast<int32_t>((__umulhi(m, static_cast<uint32_t>(n)) + static_cast<uint32_t>(n)) >> l);
+  }
+};
+
 // One layer's cache: page p holds, for each head, `page_size` slots of
 // `head_dim` elements; pages lie `page_stride` elements apart (any 64-bit
-// distance), scales [pages][heads][slots] are packed.
+// distance), `page_rows` rows of head_dim elements; scales
+// [pages][heads][slots] are packed.
 struct View {
   void* k;
   void* v;
@@ -27,6 +38,8 @@ struct View {
   int32_t* lengths;
   int64_t page_stride;
   int64_t ldp;
+  uint32_t page_rows;
+  Divisor page;  // slots of a page
   int32_t num_pages, seqs, heads, slots_per_page, dim, capacity;
 };
 

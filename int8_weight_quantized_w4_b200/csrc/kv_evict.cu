@@ -206,9 +206,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
 
 __device__ __forceinline__ int64_t row_of(const View& c, int32_t b, int32_t h, int32_t slot, int64_t* scale,
                                           ErrorWord* err) {
-  const int32_t page = page_of(c, b, slot / c.slots_per_page, err, w4dev::K_KV_EVICT);
+  const int32_t index = c.page.quotient(slot);
+  const int32_t page = page_of(c, b, index, err, w4dev::K_KV_EVICT);
   if (page < 0) return -1;
-  const int64_t inner = int64_t(h) * c.slots_per_page + slot % c.slots_per_page;
+  const int64_t inner = int64_t(h) * c.slots_per_page + (slot - index * c.slots_per_page);
   *scale = int64_t(page) * c.heads * c.slots_per_page + inner;
   return int64_t(page) * c.page_stride + inner * c.dim;
 }

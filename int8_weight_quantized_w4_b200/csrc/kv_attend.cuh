@@ -35,6 +35,7 @@ constexpr int kWarps = 4;
 constexpr int kAttendThreads = kWarps * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 7.f;  // see the bodies: how far, to base 2, a maximum may pass its reference
 
 constexpr int kOver = 1;  // an item's own cost, in units
 
@@ -363,6 +364,7 @@ struct Ring {
   static constexpr int kStage = ((kNeed > TRIPLE * 4 ? kNeed : TRIPLE * 4) + 127) / 128 * 128;
   static constexpr int kRing = STAGES * kStage;
   static constexpr int kRows = 32 / CL;          // rows of a copy instruction
+  static constexpr uint32_t kAll = (1u << TS) - 1;  // every slot of a tile
 
   Ahead<TS> ahead;
   Entry entry;              // of the tile to be copied next
@@ -377,9 +379,9 @@ struct Ring {
   }
 
   __device__ __forceinline__ void fetch_entry(const AttendParams& p) {
-    const int32_t lane = threadIdx.x & 31, slot = ahead.tile + lane;
+    const int32_t slot = ahead.tile + static_cast<int32_t>(threadIdx.x) % TS;
     entry = {0, -1};
-    if (ahead.live && lane < TS && slot < ahead.s1) {
+    if (ahead.live && slot < ahead.s1) {
       const int32_t index = p.c.page.quotient(slot);
       entry.inner = ahead.h * p.c.slots_per_page + (slot - index * p.c.slots_per_page);
       entry.page = p.c.table[ahead.b * p.c.ldp + index];
@@ -396,7 +398,7 @@ struct Ring {
       w4dev::record_error(p.err, W4_ERR_VALUE, w4dev::K_KV_ATTEND, entry.page);
       there = false;
     }
-    const uint32_t mask = __ballot_sync(0xffffffffu, there);
+    const uint32_t mask = __ballot_sync(0xffffffffu, there) & kAll;
 #pragma unroll
     for (int i = 0; i + 1 < STAGES; ++i) held[i] = held[i + 1];
     held[STAGES - 1] = mask;
@@ -404,29 +406,42 @@ struct Ring {
       const uint32_t at = there ? static_cast<uint32_t>(entry.page) * p.c.page_rows + entry.inner : 0u;
       const uint32_t n16 = p.c.dim / Elem<TYPE>::kPerVec;
       const int vec = lane % CL;
+      const uint32_t to = w4dev::smem_u32(stage);
+      const uint8_t* base = static_cast<const uint8_t*>(p.c.k) + vec * 16;
+      const int64_t v_off = static_cast<const uint8_t*>(p.c.v) - static_cast<const uint8_t*>(p.c.k);
+      if (mask == kAll && n16 == CL * CV) {
 #pragma unroll
-      for (int i = 0; i < TS / kRows; ++i) {
-        const int row = i * kRows + lane / CL;
-        const uint64_t from = uint64_t(__shfl_sync(0xffffffffu, at, row)) * (n16 * 16) + vec * 16;
-        const uint8_t* k = static_cast<const uint8_t*>(p.c.k) + from;
-        const uint8_t* v = static_cast<const uint8_t*>(p.c.v) + from;
-        const bool copy = (mask >> row) & 1u;
+        for (int i = 0; i < TS / kRows; ++i) {
+          const int row = i * kRows + lane / CL;
+          const uint8_t* k = base + uint64_t(__shfl_sync(0xffffffffu, at, row)) * (n16 * 16);
 #pragma unroll
-        for (int j = 0; j < CV; ++j) {
-          const bool in = copy && vec + j * CL < n16;  // else zeros are written, and nothing read
-          const int to = place(row, vec + j * CL);
-          w4dev::cp_async_16(stage + to, in ? k + j * CL * 16 : p.c.k, in ? 16 : 0);
-          w4dev::cp_async_16(stage + kSide + to, in ? v + j * CL * 16 : p.c.v, in ? 16 : 0);
+          for (int j = 0; j < CV; ++j) {
+            copy16(to + place(row, vec + j * CL), k + j * CL * 16, 16);
+            copy16(to + kSide + place(row, vec + j * CL), k + v_off + j * CL * 16, 16);
+          }
+        }
+      } else {  // zeros for slots that are not there and behind the row's end: nothing is read for them
+#pragma unroll 1
+        for (int i = 0; i < TS / kRows; ++i) {
+          const int row = i * kRows + lane / CL;
+          const uint8_t* k = base + uint64_t(__shfl_sync(0xffffffffu, at, row)) * (n16 * 16);
+          const bool copy = (mask >> row) & 1u;
+#pragma unroll
+          for (int j = 0; j < CV; ++j) {
+            const bool in = copy && vec + j * CL < n16;
+            const uint8_t* from = in ? k + j * CL * 16 : static_cast<const uint8_t*>(p.c.k);
+            copy16(to + place(row, vec + j * CL), from, in ? 16 : 0);
+            copy16(to + kSide + place(row, vec + j * CL), from + v_off, in ? 16 : 0);
+          }
         }
       }
-      if constexpr (I8) {
-        // lanes 0..TS-1 hold the rows; scales of keys, then of values
-        const int64_t scale = int64_t(entry.page) * (p.c.heads * p.c.slots_per_page) + entry.inner;
-        if (lane < TS) {
-          float* to = reinterpret_cast<float*>(stage + kScales);
-          copy4(to + lane, there ? p.c.ks + scale : p.c.ks, there);
-          copy4(to + TS + lane, there ? p.c.vs + scale : p.c.vs, there);
-        }
+      if constexpr (I8) {  // a lane's key scale, or from lane TS on its value scale
+        const float* scales = lane < TS ? p.c.ks : p.c.vs;
+        if (there) scales += int64_t(entry.page) * (p.c.heads * p.c.slots_per_page) + entry.inner;
+        if (lane < 2 * TS)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + kScales + 4 * lane), "l"(scales),
+                       "r"(there ? 4 : 0)
+                       : "memory");
       }
     }
     w4dev::cp_async_commit();
@@ -434,9 +449,8 @@ struct Ring {
     fetch_entry(p);
   }
 
-  __device__ static __forceinline__ void copy4(float* dst, const float* src, bool there) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(w4dev::smem_u32(dst)), "l"(src), "r"(there ? 4 : 0)
-                 : "memory");
+  __device__ static __forceinline__ void copy16(uint32_t to, const uint8_t* from, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
   }
 
   __device__ __forceinline__ void begin(const AttendParams& p, const Run& run, const Walk& w, uint8_t* own) {
@@ -541,11 +555,18 @@ struct PlainLanes {
           for (int o = 1; o < LPR; o *= 2) x[g][i] += __shfl_xor_sync(0xffffffffu, x[g][i], o);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const bool there = (held >> (i * RPW + rg)) & 1u;
         float f = p.scale2;
         if constexpr (TYPE == W4_KV_I8) f *= scales[i * RPW + rg];
 #pragma unroll
-        for (int g = 0; g < GT; ++g) x[g][i] = there ? x[g][i] * f : -INFINITY;
+        for (int g = 0; g < GT; ++g) x[g][i] *= f;
+      }
+      if (held != Feed::kAll) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const bool there = (held >> (i * RPW + rg)) & 1u;
+#pragma unroll
+          for (int g = 0; g < GT; ++g) x[g][i] = there ? x[g][i] : -INFINITY;
+        }
       }
       if (p.scores != nullptr) {
 #pragma unroll
@@ -562,7 +583,8 @@ struct PlainLanes {
         float top = m[g];
 #pragma unroll
         for (int i = 0; i < NP; ++i) top = fmaxf(top, x[g][i]);
-        if (top > m[g]) {
+        // the reference follows the maximum once it lies kSlack below: weights of up to 2^kSlack are as good
+        if (top > m[g] + kSlack) {
           if (m[g] != -INFINITY) {
             const float f = ex2(m[g] - top);
             l[g] *= f;
@@ -571,7 +593,7 @@ struct PlainLanes {
           }
           m[g] = top;
         }
-        const float ref = top == -INFINITY ? 0.f : top;
+        const float ref = m[g] == -INFINITY ? 0.f : m[g];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           x[g][i] = ex2(x[g][i] - ref);

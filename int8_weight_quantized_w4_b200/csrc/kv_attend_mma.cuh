@@ -7,9 +7,10 @@
 // pieces of that type, which lie in different rows of the 16-row A operand
 // and are added up in fp32 behind the product:
 //   fp16, int8: 8 heads x 2 pieces, 11 + 11 bits: the second one holds the
-//               exact rest, scaled by 2^11. Queries and weights are scaled by
-//               powers of two so that their largest lies at 2^14: what is left
-//               out is below 2^-22 of each of them or 2^-50 of the largest;
+//               exact rest, scaled by 2^11. Queries are scaled by a power of
+//               two so that their largest lies at 2^14, weights so that it lies
+//               from 2^7 to 2^14: what is left out is below 2^-22 of each of
+//               them or 2^-43 of the largest;
 //   bf16:       4 heads x 3 pieces (8 + 8 + 8 bits, all of them) in one
 //               instruction, or 8 heads in two (pieces 0 and 1, then 2).
 //
@@ -98,7 +99,8 @@ struct MatrixLanes {
   static constexpr int NC = (MAXD / VE + 7) / 8;        // value vectors of a lane
   static constexpr int NT = 1;                          // tiles of 16 slots at once
   static constexpr int TS = 16 * NT;
-  static constexpr int kLift = BF ? 0 : 14;  // fp16 pieces: the exponent of the largest value
+  static constexpr int kLift = 14;  // fp16 pieces: the exponent of the largest query, and of the largest weight
+  static constexpr float kBelow = BF ? 0.f : kLift - kSlack;  // a new reference lies this far below the maximum
   static constexpr int kFrag = SETS * STEPS * 32 * 4;   // words of the queries' operands
   static constexpr int kWidth = MAXD;  // of a row of queries in shared memory
   static constexpr int kBodyFloats = kFrag;
@@ -233,10 +235,19 @@ struct MatrixLanes {
           const int slot = 8 * n + 2 * t + e;
           float f = scale;
           if constexpr (I8) f *= scales[slot];
-          const float v = joined(c[n][e], c[n][2 + e]) * f;
-          x[n][e] = (held >> slot) & 1u ? v : -INFINITY;
-          top = fmaxf(top, x[n][e]);
+          x[n][e] = joined(c[n][e], c[n][2 + e]) * f;
         }
+      if (held != Feed::kAll) {
+#pragma unroll
+        for (int n = 0; n < 2 * NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (!((held >> (8 * n + 2 * t + e)) & 1u)) x[n][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int n = 0; n < 2 * NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) top = fmaxf(top, x[n][e]);
       if (p.scores != nullptr && head < seg.ng && g < ROWS) {
         float* to = p.scores + (int64_t(seg.b) * p.c.heads * p.group + seg.q0 + head) * p.c.capacity + tile + 2 * t;
 #pragma unroll
@@ -247,11 +258,15 @@ struct MatrixLanes {
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // weights are 2^(x - m), the largest 2^kLift: the triple's m lies that far below its scores
-      top = fmaxf(m, top - kLift);
-      float back = m == -INFINITY ? 1.f : ex2(m - top);  // without a score so far there are zeros, or a NaN
-      l *= back;
-      m = top;
+      // weights are 2^(x - m): m follows the maximum when that passes it by more
+      // than what keeps the largest weight below 2^kLift
+      float back = 1.f;
+      if (top - kBelow > m + kSlack) {
+        top -= kBelow;
+        if (m != -INFINITY) back = ex2(m - top);  // without a score so far there are zeros, or a NaN
+        l *= back;
+        m = top;
+      }
       float unit = 1.f;
       if constexpr (I8) {
         const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(scales[TS + lane % TS]))) >> 23);

@@ -53,9 +53,10 @@ def kv_attend_ref(q, k, v, scale: float, window: int = 0):
     rest is at most 2^-11 of it and exact in fp32, the second one (that rest
     times 2^11) is off by at most 2^-11 of the rest, or by half of fp16's
     smallest step, 2^-25, which is 2^-36 of what is stored. So 2^-22 of each
-    term is left out, or 2^-36 where the largest is at least 2^14: 2^-50 of
-    the largest q, and of the largest weight times the largest int8 scale
-    (twice that, a scale lies up to 2 above its power of two). A weight is the exponential
+    term is left out, or 2^-36, where the largest q is at least 2^14 and the
+    largest weight at least 2^7: 2^-50 of the largest q, 2^-43 of the largest
+    weight, times the largest int8 scale (twice that, a scale lies up to 2
+    above its power of two). A weight is the exponential
     of a difference of two scores (the exponential itself is good to 2^-22),
     and sums of n weights, in any order, rescaled at most once a slot, lose at
     most 2 n roundings."""
@@ -79,7 +80,7 @@ def kv_attend_ref(q, k, v, scale: float, window: int = 0):
         ds = ((D + 4) * EPS + 2.0 ** -21) * abs(scale) * (np.abs(kk) @ np.abs(q[i])).max() + 4 * EPS * np.abs(s).max()
         ds += 2.0 ** -50 * abs(scale) * np.abs(q[i]).max() * np.abs(kk).sum(1).max()
         rel = 2 * ds + (2 * (n - lo) + 64) * EPS
-        t_out[i] = rel * (w[i, lo:] @ np.abs(vv)) + 2.0 ** -49 * 127 * (n - lo) * np.abs(vv).max() + 1e-37
+        t_out[i] = rel * (w[i, lo:] @ np.abs(vv)) + 2.0 ** -42 * 127 * (n - lo) * np.abs(vv).max() + 1e-37
         t_lse[i] = rel + 4 * EPS * abs(lse[i])
         t_w[i, lo:] = rel * w[i, lo:] + 1e-37
     return out, lse, w, (t_out, t_lse, t_w)

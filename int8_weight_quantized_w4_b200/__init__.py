@@ -75,9 +75,9 @@ def _ptr(t) -> int:
 
 
 def _stream_handle(stream) -> int:
-    torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream()
+        torch = _torch()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream)
 
 
@@ -639,21 +639,27 @@ class _On:
     allocated inside belongs to the stream that the call runs on."""
 
     def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
         self.cuda = _torch().cuda
         self.index, self.was = device.index, self.cuda.current_device()
         self.stream = None if stream is None else self.cuda.stream(stream)
 
     def __enter__(self):
-        if self.index != self.was:
-            self.cuda.set_device(self.index)
+        self.cuda.set_device(self.index)
         if self.stream is not None:
             self.stream.__enter__()
 
     def __exit__(self, *exc):
         if self.stream is not None:
             self.stream.__exit__(*exc)
-        if self.index != self.was:
-            self.cuda.set_device(self.was)
+        self.cuda.set_device(self.was)
+
+
+def _elsewhere(device, stream) -> bool:
+    """Whether a call has to be made inside _On: another stream than the
+    current one is asked for, or the tensors' device is not the current one."""
+    return stream is not None or _torch().cuda.current_device() != device.index
 
 
 def kv_append(cache: KvCache, k, v, cu_tokens=None, lengths_out=None, stream=None):
@@ -662,8 +668,10 @@ def kv_append(cache: KvCache, k, v, cu_tokens=None, lengths_out=None, stream=Non
     cu_tokens[b] .. cu_tokens[b + 1] - 1 (int32 [seqs + 1]) to sequence b, or
     one row each without cu_tokens. The lengths advance in place, or go to
     lengths_out (int32 [seqs]); returns them."""
-    torch = _torch()
-    dev = cache.device
+    torch, dev = _torch(), cache.device
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return kv_append(cache, k, v, cu_tokens, lengths_out)
     n = k.shape[0]
     ldk = _rows3(k, "k", None, cache.kv_heads, cache.head_dim, dev)
     ldv = _rows3(v, "v", n, cache.kv_heads, cache.head_dim, dev)
@@ -671,9 +679,9 @@ def kv_append(cache: KvCache, k, v, cu_tokens=None, lengths_out=None, stream=Non
     if lengths_out is None:
         lengths_out = cache.lengths
     out = _vector(lengths_out, "lengths_out", torch.int32, cache.seqs, dev)
-    with _On(dev, stream):
-        _check(lib().kv_append(cache._ref, k.data_ptr(), ldk, v.data_ptr(), ldv, cu, n, out, _stream_handle(stream)),
-               "kv_append")
+    st = lib().kv_append(cache._ref, k.data_ptr(), ldk, v.data_ptr(), ldv, cu, n, out, _stream_handle(None))
+    if st != 0:
+        _check(st, "kv_append")
     return lengths_out
 
 
@@ -684,30 +692,32 @@ def kv_attend(q, cache: KvCache, scale: float | None = None, window: int = 0, ou
     `window` of them when it is positive; scale defaults to head_dim ** -0.5.
     lse: fp32 [seqs, q_heads], filled. acc: fp32 [seqs, >= capacity], each
     slot's weight summed over the query heads is added."""
-    torch = _torch()
-    dev, B, D = cache.device, cache.seqs, cache.head_dim
+    torch, dev, B, D = _torch(), cache.device, cache.seqs, cache.head_dim
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return kv_attend(q, cache, scale, window, out, lse, acc, ws)
     ldq = _rows3(q, "q", B, None, D, dev)
     Hq = q.shape[1]
     ldo = Hq * D if out is None else _rows3(out, "out", B, Hq, D, dev)
-    if lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != (B, Hq) or
-                            not lse.is_contiguous() or lse.device != dev):
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous() or
+                            lse.device != dev):
         raise ValueError(f"lse must be a contiguous fp32 [{B}, {Hq}] tensor on {dev}")
     ldacc = 0 if acc is None else _matrix(acc, "acc", torch.float32, B, cache.capacity, dev)
-    with _On(dev, stream):
-        key = (Hq, acc is not None)
-        need = cache._need.get(key)
-        if need is None:
-            need = cache._need[key] = int(lib().kv_attend_workspace_size(cache._ref, Hq, int(acc is not None)))
-        if out is None:
-            out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
-        # torch hands the workspace out again only behind this call on its
-        # stream, and a captured call's belongs to its graph
-        if ws is None and need:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        _check(lib().kv_attend(cache._ref, q.data_ptr(), ldq, Hq, D ** -0.5 if scale is None else scale, window,
-                               out.data_ptr(), ldo, _ptr(lse), _ptr(acc), ldacc, _ptr(ws),
-                               0 if ws is None else ws.numel() * ws.element_size(), _stream_handle(stream)),
-               "kv_attend")
+    key = (Hq, acc is not None)
+    need = cache._need.get(key)
+    if need is None:
+        need = cache._need[key] = int(lib().kv_attend_workspace_size(cache._ref, Hq, int(acc is not None)))
+    if out is None:
+        out = torch.empty(B, Hq, D, dtype=torch.float32, device=dev)
+    # torch hands the workspace out again only behind this call on its stream,
+    # and a captured call's belongs to its graph
+    if ws is None and need:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    st = lib().kv_attend(cache._ref, q.data_ptr(), ldq, Hq, D ** -0.5 if scale is None else scale, window,
+                         out.data_ptr(), ldo, _ptr(lse), _ptr(acc), ldacc, _ptr(ws),
+                         0 if ws is None else ws.numel() * ws.element_size(), _stream_handle(None))
+    if st != 0:
+        _check(st, "kv_attend")
     return out
 
 
@@ -719,8 +729,10 @@ def kv_evict(cache: KvCache, acc, keep: int, recent: int = 0, dst: KvCache | Non
     in place or into dst (a cache of other pages); acc moves along, in place
     or into acc_out. kept: int32 [seqs, >= keep], filled with the kept slots'
     old places and -1. Returns the new lengths."""
-    torch = _torch()
-    dev, B = cache.device, cache.seqs
+    torch, dev, B = _torch(), cache.device, cache.seqs
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return kv_evict(cache, acc, keep, recent, dst, acc_out, kept, ws)
     if dst is None:
         dst = cache
     elif dst.device != dev:
@@ -730,13 +742,13 @@ def kv_evict(cache: KvCache, acc, keep: int, recent: int = 0, dst: KvCache | Non
     ld = _matrix(acc, "acc", torch.float32, B, cache.capacity, dev)
     ldo = _matrix(acc_out, "acc_out", torch.float32, B, cache.capacity, dev)
     ldk = 0 if kept is None else _matrix(kept, "kept", torch.int32, B, keep, dev)
-    with _On(dev, stream):
-        need = int(lib().kv_evict_workspace_size(cache._ref, keep))
-        if ws is None and need:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        _check(lib().kv_evict(cache._ref, acc.data_ptr(), ld, keep, recent, dst._ref, acc_out.data_ptr(), ldo,
-                              _ptr(kept), ldk, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-                              _stream_handle(stream)), "kv_evict")
+    need = int(lib().kv_evict_workspace_size(cache._ref, keep))
+    if ws is None and need:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    st = lib().kv_evict(cache._ref, acc.data_ptr(), ld, keep, recent, dst._ref, acc_out.data_ptr(), ldo, _ptr(kept),
+                        ldk, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream_handle(None))
+    if st != 0:
+        _check(st, "kv_evict")
     return dst.lengths
 
 
@@ -747,26 +759,33 @@ def token_logprobs(logits, tokens=None, top: int = 0, stream=None):
     tokens (int32 [M], -1 scores nothing), entropy [M], the `top` best tokens'
     top_logp [M, top] and top_ids int32 [M, top], best first). logp is None
     without tokens, the last two without top."""
-    torch = _torch()
-    if logits.dim() == 1:
-        logits = logits.view(1, -1)
-    M, V = logits.shape
-    dev = logits.device
+    torch, dev = _torch(), logits.device
     if not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor")
-    ld = _matrix(logits, "logits", torch.float32, M, V, dev)
-    t = 0 if tokens is None else _vector(tokens, "tokens", torch.int32, M, dev)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return token_logprobs(logits, tokens, top)
+    if logits.dim() == 1:
+        logits = logits.view(1, -1)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [M, V]")
+    M, V = logits.shape
+    f32 = torch.float32
+    ld = _matrix(logits, "logits", f32, M, V, dev)
+    t = lp = tl = ti = 0
     logp = top_logp = top_ids = None
-    f32 = {"dtype": torch.float32, "device": dev}
-    with _On(dev, stream):
-        if tokens is not None:
-            logp = torch.empty(M, **f32)
-        entropy = torch.empty(M, **f32)
-        if top > 0:
-            top_logp = torch.empty((M, top), **f32)
-            top_ids = torch.empty((M, top), dtype=torch.int32, device=dev)
-        _check(lib().token_logprobs(logits.data_ptr(), ld, t, M, V, top, _ptr(logp), entropy.data_ptr(),
-                                    _ptr(top_logp), _ptr(top_ids), _stream_handle(stream)), "token_logprobs")
+    if tokens is not None:
+        t = _vector(tokens, "tokens", torch.int32, M, dev)
+        logp = torch.empty(M, dtype=f32, device=dev)
+        lp = logp.data_ptr()
+    entropy = torch.empty(M, dtype=f32, device=dev)
+    if top > 0:
+        top_logp = torch.empty(M, top, dtype=f32, device=dev)
+        top_ids = torch.empty(M, top, dtype=torch.int32, device=dev)
+        tl, ti = top_logp.data_ptr(), top_ids.data_ptr()
+    st = lib().token_logprobs(logits.data_ptr(), ld, t, M, V, top, lp, entropy.data_ptr(), tl, ti, _stream_handle(None))
+    if st != 0:
+        _check(st, "token_logprobs")
     return logp, entropy, top_logp, top_ids
 
 

@@ -22,13 +22,13 @@ using namespace w4kv;
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kMostUnits = 4;
 constexpr int kMaxLaneVecs = 2;  // float4s of a lane: 32 x 4 x 2 = 256, the largest head_dim
 
 // One query head per `wpr` warps: wpr = 8 spreads the partials of a few long
 // rows, wpr = 1 passes over many rows that mostly have nothing to join.
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p, int wpr) {
-  __shared__ float4 sm_a[kJoinWarps][32 * kMaxLaneVecs];
-  __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
+  __shared__ Triple sm[kJoinWarps][32 * kMaxLaneVecs];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -36,10 +36,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
   const int64_t row = int64_t(blockIdx.x) * (kJoinWarps / wpr) + warp / wpr;
   const int sub = warp % wpr;
   const int D = p.c.dim, vecs = D / 4;
-  float m = -INFINITY, l = 0.f;
-  float4 a[kMaxLaneVecs];
+  Triple x[kMaxLaneVecs];
 #pragma unroll
-  for (int i = 0; i < kMaxLaneVecs; ++i) a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < kMaxLaneVecs; ++i) x[i] = no_slots();
   bool work = false;
   int32_t b = 0, qh = 0;
   if (row < int64_t(p.c.seqs) * q_heads) {
@@ -55,60 +54,25 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
       // the first partial, then the next CTAs' first ones
       const int64_t slot = i == 0 ? meta.x : 2 * int64_t(meta.x / 2 + i);
       const float* part = p.part + slot * p.part_stride;
-      const float pm = part[p.rows * D + g], pl = part[p.rows * D + p.rows + g];
-      const float top = fmaxf(m, pm);
-      const float f = m == -INFINITY ? 1.f : ex2(m - top), pf = pm == -INFINITY ? 1.f : ex2(pm - top);
-      m = top;
-      l = l * f + pl * pf;
 #pragma unroll
-      for (int j = 0; j < kMaxLaneVecs; ++j) {
-        if (lane + 32 * j < vecs) {
-          const float4 x = *reinterpret_cast<const float4*>(part + g * D + 4 * (lane + 32 * j));
-          a[j] = make_float4(a[j].x * f + x.x * pf, a[j].y * f + x.y * pf, a[j].z * f + x.z * pf,
-                             a[j].w * f + x.w * pf);
-        }
-      }
+      for (int j = 0; j < kMaxLaneVecs; ++j)
+        if (lane + 32 * j < vecs) join(x[j], stored(part, p.rows, D, g, 4 * (lane + 32 * j)));
     }
   }
   if (wpr > 1) {
-    if (lane == 0) {
-      sm_m[warp] = m;
-      sm_l[warp] = l;
-    }
 #pragma unroll
-    for (int j = 0; j < kMaxLaneVecs; ++j) sm_a[warp][lane + 32 * j] = a[j];
+    for (int j = 0; j < kMaxLaneVecs; ++j) sm[warp][lane + 32 * j] = x[j];
     __syncthreads();
     if (sub != 0) return;
     for (int w = warp + 1; w < warp + wpr; ++w) {
-      const float pm = sm_m[w];
-      const float top = fmaxf(m, pm);
-      const float f = m == -INFINITY ? 1.f : ex2(m - top), pf = pm == -INFINITY ? 1.f : ex2(pm - top);
-      m = top;
-      l = l * f + sm_l[w] * pf;
 #pragma unroll
-      for (int j = 0; j < kMaxLaneVecs; ++j) {
-        const float4 x = sm_a[w][lane + 32 * j];
-        a[j] = make_float4(a[j].x * f + x.x * pf, a[j].y * f + x.y * pf, a[j].z * f + x.z * pf, a[j].w * f + x.w * pf);
-      }
+      for (int j = 0; j < kMaxLaneVecs; ++j) join(x[j], sm[w][lane + 32 * j]);
     }
   }
   if (!work) return;
-  const bool none = l == 0.f;
 #pragma unroll
-  for (int j = 0; j < kMaxLaneVecs; ++j) {
-    if (lane + 32 * j < vecs) {
-      float* o = p.out + b * p.ldo + int64_t(qh) * D + 4 * (lane + 32 * j);
-      o[0] = none ? 0.f : a[j].x / l;
-      o[1] = none ? 0.f : a[j].y / l;
-      o[2] = none ? 0.f : a[j].z / l;
-      o[3] = none ? 0.f : a[j].w / l;
-    }
-  }
-  if (lane == 0) {
-    const float z = none ? -INFINITY : m + log2f(l);
-    if (p.lse != nullptr) p.lse[row] = z * kLn2;
-    if (p.lse2 != nullptr) p.lse2[row] = z;
-  }
+  for (int j = 0; j < kMaxLaneVecs; ++j)
+    if (lane + 32 * j < vecs) write_out(p, b, qh, 4 * (lane + 32 * j), x[j]);
 }
 
 // acc[b, j] += sum over the query heads of 2^(x - lse2), heads in order.
@@ -134,6 +98,7 @@ __global__ void __launch_bounds__(kJoinThreads) gather_kernel(const AttendParams
 struct Layout {
   AttendKernel kernel;
   int32_t chunks;
+  unsigned ranks;  // CTAs of an item's cluster; 0: runs of units, and a join
   unsigned ctas;
   int64_t part_stride;
   size_t meta, lse2, scores, bytes;  // offsets, and the total
@@ -167,6 +132,9 @@ w4_status resident(const AttendKernel& k, int* out) {
   int n = 0;
   cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
   if (e != cudaSuccess) return w4host::cuda_fail(e, "kv_attend shared memory");
+  e = cudaFuncSetAttribute(k.item_fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k.item_fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return w4host::cuda_fail(e, "kv_attend cluster size");
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k.fn, kAttendThreads, k.smem);
   if (e != cudaSuccess) return w4host::cuda_fail(e, "kv_attend occupancy");
   if (n < 1) return w4host::fail(W4_ERR_CUDA, "kv_attend: no CTA fits an SM");
@@ -187,7 +155,23 @@ w4_status lay_out(const w4kv::View& c, int type, int64_t q_heads, bool with_acc,
   const int64_t items = int64_t(c.seqs) * c.heads * L.chunks;
   const int64_t most = items * ((c.capacity + L.kernel.unit - 1) / L.kernel.unit + kOver);
   if (most > 0x7fffffff) return w4host::fail(W4_ERR_SHAPE, "seqs x heads x capacity are more slots than a call takes");
-  L.ctas = static_cast<unsigned>(most < int64_t(per_sm) * sms ? (most > 0 ? most : 1) : int64_t(per_sm) * sms);
+  const int64_t wave = int64_t(per_sm) * sms;
+  // An item a cluster: the widest of up to 16 CTAs that one wave holds for all
+  // items, where it leaves a CTA kMostUnits units of a full sequence. One
+  // 12 x 64 sequence of 1021 slots: 6.6 us against 9.1 us as runs and a join.
+  const int64_t units = (c.capacity + L.kernel.unit - 1) / L.kernel.unit;
+  unsigned ranks = 16;
+  while (ranks > 1 && (items * ranks > wave || ranks / 2 >= units)) ranks /= 2;
+  L.ranks = items * ranks <= wave && units <= int64_t(kMostUnits) * ranks ? ranks : 0;
+  if (L.ranks != 0) {
+    L.ctas = static_cast<unsigned>(items * ranks);
+    L.lse2 = 0;
+    L.scores = with_acc ? round256(static_cast<size_t>(c.seqs) * q_heads * 4) : 0;
+    L.bytes = L.scores + (with_acc ? static_cast<size_t>(c.seqs) * q_heads * c.capacity * 4 : 0);
+    *out = L;
+    return W4_OK;
+  }
+  L.ctas = static_cast<unsigned>(most < wave ? (most > 0 ? most : 1) : wave);
   L.part_stride = (int64_t(L.kernel.rows) * (c.dim + 2) + 3) / 4 * 4;
   L.meta = round256(size_t(2) * L.ctas * L.part_stride * 4);
   L.lse2 = L.meta + round256(static_cast<size_t>(items) * sizeof(int2));
@@ -242,7 +226,7 @@ extern "C" w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, i
   Layout L;
   rc = lay_out(p.c, c->type, q_heads, acc != nullptr, di->sms, &L);
   if (rc != W4_OK) return rc;
-  if (workspace == nullptr || workspace_bytes < L.bytes)
+  if (L.bytes > 0 && (workspace == nullptr || workspace_bytes < L.bytes))
     return fail(W4_ERR_WORKSPACE, "kv_attend needs a workspace of %zu bytes, %zu given", L.bytes,
                 workspace == nullptr ? size_t(0) : workspace_bytes);
   if (bits(workspace) & 15) return fail(W4_ERR_WORKSPACE, "workspace must be 16-byte aligned");
@@ -268,18 +252,23 @@ extern "C" w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, i
   p.chunks = L.chunks;
   p.err = di->err;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(L.kernel.fn, dim3(L.ctas), kAttendThreads, L.kernel.smem, st, p);
+  cudaError_t e;
+  if (L.ranks != 0) {
+    e = launch_pdl(L.kernel.item_fn, dim3(L.ctas), kAttendThreads, L.kernel.smem, st, L.ranks, p);
+  } else {
+    e = launch_pdl(L.kernel.fn, dim3(L.ctas), kAttendThreads, L.kernel.smem, st, 1, p);
+    if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend");
+    const int64_t rows = c->seqs * q_heads;
+    const int wpr = rows <= int64_t(di->sms) * kJoinWarps ? kJoinWarps : 1;
+    const int64_t rows_per_cta = kJoinWarps / wpr;
+    e = launch_pdl(join_kernel, dim3(static_cast<unsigned>((rows + rows_per_cta - 1) / rows_per_cta)), kJoinThreads, 0,
+                   st, 1, p, wpr);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend");
-  const int64_t rows = c->seqs * q_heads;
-  const int wpr = rows <= int64_t(di->sms) * kJoinWarps ? kJoinWarps : 1;
-  const int64_t rows_per_cta = kJoinWarps / wpr;
-  e = launch_pdl(join_kernel, dim3(static_cast<unsigned>((rows + rows_per_cta - 1) / rows_per_cta)), kJoinThreads, 0, st,
-                 p, wpr);
-  if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend (join)");
   if (acc != nullptr && p.c.capacity > 0) {
     const int64_t per_row = (p.c.capacity + kJoinThreads - 1) / kJoinThreads;
     const dim3 grid(static_cast<unsigned>(per_row < 512 ? per_row : 512), static_cast<unsigned>(c->seqs));
-    e = launch_pdl(gather_kernel, grid, kJoinThreads, 0, st, p, acc, ldacc);
+    e = launch_pdl(gather_kernel, grid, kJoinThreads, 0, st, 1, p, acc, ldacc);
     if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend (weights)");
   }
   return W4_OK;

@@ -18,7 +18,9 @@
 // CTA holds at most one item that began before its run and one that goes on
 // behind it; those leave (m, l, a) in the workspace and join_kernel joins them
 // in the order of the slots. So no result depends on timing, and nothing has
-// to be zero beforehand.
+// to be zero beforehand. Where one wave of clusters holds all items with a few
+// units for each CTA, an item is a cluster instead, and its CTAs join theirs
+// through shared memory: one launch, no workspace traffic.
 //
 // Latency. Each warp feeds itself: its tiles of 4 to 16 slots follow one another
 // across the segments of its CTA's run, and while it works on one the next
@@ -27,9 +29,13 @@
 // they belong to; their entries of the page table were fetched a tile earlier.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include "kv_cache.cuh"
 
 namespace w4kv {
+
+namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
 constexpr int kAttendThreads = kWarps * 32;
@@ -259,52 +265,78 @@ struct Queries {
   }
 };
 
-// The four warps' triples of a segment (a [ROWS][dim], m [ROWS], l [ROWS], each
-// in a stage of the warp's ring) joined, and written: the result, or a partial.
+// (a, m, l) of one quad of a query head's sums.
+struct Triple {
+  float4 a;
+  float m, l;
+};
+
+__device__ __forceinline__ Triple no_slots() { return {make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f}; }
+
+// b into a. A triple without a score (m = -Inf) holds zeros, or a NaN that stays one.
+__device__ __forceinline__ void join(Triple& a, const Triple& b) {
+  const float m = fmaxf(a.m, b.m);
+  const float f = a.m == -INFINITY ? 1.f : ex2(a.m - m), g = b.m == -INFINITY ? 1.f : ex2(b.m - m);
+  a.a = make_float4(a.a.x * f + b.a.x * g, a.a.y * f + b.a.y * g, a.a.z * f + b.a.z * g, a.a.w * f + b.a.w * g);
+  a.l = a.l * f + b.l * g;
+  a.m = m;
+}
+
+// A stored triple's quad: a [rows][dim], m [rows], l [rows].
+__device__ __forceinline__ Triple stored(const float* t, int rows, int D, int g, int d) {
+  return {*reinterpret_cast<const float4*>(t + g * D + d), t[rows * D + g], t[rows * D + rows + g]};
+}
+
+__device__ __forceinline__ void store(float* t, int rows, int D, int g, int d, const Triple& x) {
+  *reinterpret_cast<float4*>(t + g * D + d) = x.a;
+  if (d == 0) {
+    t[rows * D + g] = x.m;
+    t[rows * D + rows + g] = x.l;
+  }
+}
+
+// The result of a whole item's quad, query head q of sequence b.
+__device__ __forceinline__ void write_out(const AttendParams& p, int32_t b, int32_t q, int d, const Triple& x) {
+  float* o = p.out + b * p.ldo + int64_t(q) * p.c.dim + d;
+  const float by = x.l == 0.f ? 0.f : 1.f / x.l;  // no slot with a weight: a is 0 too
+  o[0] = x.a.x * by;
+  o[1] = x.a.y * by;
+  o[2] = x.a.z * by;
+  o[3] = x.a.w * by;
+  if (d == 0) {
+    const float z = x.l == 0.f ? -INFINITY : x.m + log2f(x.l);
+    const int64_t at = int64_t(b) * p.c.heads * p.group + q;
+    if (p.lse != nullptr) p.lse[at] = z * kLn2;
+    if (p.lse2 != nullptr) p.lse2[at] = z;
+  }
+}
+
+// The four warps' triples of a segment (each in a stage of the warp's ring)
+// joined, quad by quad: sink(g, d, triple).
+template <int ROWS, class Sink>
+__device__ __forceinline__ void join_warps(const AttendParams& p, int ng, float* const (&triple)[kWarps], Sink sink) {
+  const int D = p.c.dim, quads = D / 4;
+  for (int i = threadIdx.x; i < ng * quads; i += kAttendThreads) {
+    const int g = i / quads, d = 4 * (i - g * quads);
+    Triple x = stored(triple[0], ROWS, D, g, d);
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) join(x, stored(triple[w], ROWS, D, g, d));
+    sink(g, d, x);
+  }
+}
+
+// A segment's result, or partial.
 template <int ROWS>
 __device__ __forceinline__ void finish(const AttendParams& p, const Segment& s, bool first, float* const (&triple)[kWarps]) {
-  const int D = p.c.dim;
   const int64_t slot = 2 * int64_t(blockIdx.x) + (first ? 0 : 1);
   float* part = p.part + slot * p.part_stride;
-  const int quads = D / 4;
-  for (int i = threadIdx.x; i < s.ng * quads; i += kAttendThreads) {
-    const int g = i / quads, d = 4 * (i - g * quads);
-    float m[kWarps], M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      m[w] = triple[w][ROWS * D + g];
-      M = fmaxf(M, m[w]);
-    }
-    float l = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = m[w] == -INFINITY ? 1.f : ex2(m[w] - M);  // a warp without a score holds zeros, or a NaN
-      const float4 x = *reinterpret_cast<const float4*>(triple[w] + g * D + d);
-      l = fmaf(triple[w][ROWS * D + ROWS + g], f, l);
-      a = make_float4(fmaf(x.x, f, a.x), fmaf(x.y, f, a.y), fmaf(x.z, f, a.z), fmaf(x.w, f, a.w));
-    }
+  join_warps<ROWS>(p, s.ng, triple, [&](int g, int d, const Triple& x) {
     if (s.whole) {
-      float* o = p.out + s.b * p.ldo + int64_t(s.q0 + g) * D + d;
-      const float by = l == 0.f ? 0.f : 1.f / l;  // no slot with a weight: a is 0 too
-      o[0] = a.x * by;
-      o[1] = a.y * by;
-      o[2] = a.z * by;
-      o[3] = a.w * by;
-      if (d == 0) {
-        const float z = l == 0.f ? -INFINITY : M + log2f(l);
-        const int64_t at = int64_t(s.b) * p.c.heads * p.group + s.q0 + g;
-        if (p.lse != nullptr) p.lse[at] = z * kLn2;
-        if (p.lse2 != nullptr) p.lse2[at] = z;
-      }
+      write_out(p, s.b, s.q0 + g, d, x);
     } else {
-      *reinterpret_cast<float4*>(part + g * D + d) = a;
-      if (d == 0) {
-        part[p.rows * D + g] = M;
-        part[p.rows * D + p.rows + g] = l;
-      }
+      store(part, ROWS, p.c.dim, g, d, x);
     }
-  }
+  });
   if (s.count > 0 && threadIdx.x == 0)
     p.meta[int64_t(s.b) * p.c.heads * p.chunks + s.item] = make_int2(static_cast<int32_t>(slot), s.count);
 }
@@ -322,7 +354,9 @@ __device__ __forceinline__ void attend_runs(const AttendParams& p, uint8_t* smem
   if (!find_run(p, w, run, scratch)) return;
   __syncthreads();
   typename Body::Feed feed;
-  feed.begin(p, run, w, smem + (threadIdx.x >> 5) * Body::Feed::kRing);
+  feed.ahead.w = w;
+  feed.ahead.open(p, run);
+  feed.begin(p, run, smem + (threadIdx.x >> 5) * Body::Feed::kRing);
   Segment s = {}, prev = {};
   for (int k = 0;; ++k) {
     const bool more = next_segment(p, run, w, s);
@@ -339,6 +373,66 @@ __device__ __forceinline__ void attend_runs(const AttendParams& p, uint8_t* smem
     if ((threadIdx.x & 31) == 0) triple[threadIdx.x >> 5] = to;
     prev = s;
   }
+}
+
+// One item by a cluster: each CTA takes an equal share of its units, and their
+// triples meet in shared memory.
+template <class Body, int ROWS>
+__device__ __forceinline__ void attend_item(const AttendParams& p, uint8_t* smem) {
+  __shared__ float* triple[kWarps];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
+  float* sq = reinterpret_cast<float*>(smem + kWarps * Body::Feed::kRing);
+  float* body = sq + ROWS * Body::kWidth;
+  float* mine = body + Body::kBodyFloats;  // this CTA's triple
+  const int32_t item = blockIdx.x / ranks, items = p.c.heads * p.chunks;
+  const int D = p.c.dim;
+  int32_t lo, n;
+  Segment s = {};
+  s.b = item / items;
+  s.item = item - s.b * items;
+  attended(p, s.b, lo, n);
+  const int32_t units = units_of(p, n - lo);
+  const int32_t from = units * rank / ranks, to = units * (rank + 1) / ranks;
+  s.h = s.item / p.chunks;
+  const int32_t g0 = (s.item - s.h * p.chunks) * p.rows;
+  s.q0 = s.h * p.group + g0;
+  s.ng = min(p.rows, p.group - g0);
+  s.s0 = lo + (from << p.unit_log);
+  s.s1 = min(n, lo + (to << p.unit_log));
+  const Run run = {};  // not asked: the walk holds no further unit
+  typename Body::Feed feed;
+  feed.ahead.w.left = 0;
+  feed.ahead.b = s.b;
+  feed.ahead.h = s.h;
+  feed.ahead.s1 = s.s1;
+  feed.ahead.tile = s.s0 + static_cast<int32_t>(threadIdx.x >> 5) * Body::TS;
+  feed.ahead.live = feed.ahead.tile < s.s1;
+  Queries<ROWS, Body::kWidth> queries;
+  queries.fetch(p, s);
+  feed.begin(p, run, smem + (threadIdx.x >> 5) * Body::Feed::kRing);
+  queries.store(sq);
+  __syncthreads();
+  float* own = Body::segment(p, run, s, feed, sq, body);
+  if ((threadIdx.x & 31) == 0) triple[threadIdx.x >> 5] = own;
+  __syncthreads();
+  join_warps<ROWS>(p, s.ng, triple, [&](int g, int d, const Triple& x) {
+    if (ranks == 1) {
+      write_out(p, s.b, s.q0 + g, d, x);
+    } else {
+      store(mine, ROWS, D, g, d, x);
+    }
+  });
+  if (ranks == 1) return;
+  cluster.sync();
+  const int quads = D / 4;
+  for (int i = rank * kAttendThreads + threadIdx.x; i < s.ng * quads; i += ranks * kAttendThreads) {
+    const int g = i / quads, d = 4 * (i - g * quads);
+    Triple x = no_slots();
+    for (int r = 0; r < ranks; ++r) join(x, stored(cluster.map_shared_rank(mine, r), ROWS, D, g, d));
+    write_out(p, s.b, s.q0 + g, d, x);
+  }
+  cluster.sync();  // no CTA leaves while its triple is read
 }
 
 // ---------------------------------------------------------------- plain lanes
@@ -453,11 +547,10 @@ struct Ring {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
   }
 
-  __device__ __forceinline__ void begin(const AttendParams& p, const Run& run, const Walk& w, uint8_t* own) {
+  // The first tiles, once `ahead` is at the very first.
+  __device__ __forceinline__ void begin(const AttendParams& p, const Run& run, uint8_t* own) {
     ring = own;
     put = 0;
-    ahead.w = w;
-    ahead.open(p, run);
     fetch_entry(p);
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) held[i] = 0;
@@ -658,9 +751,18 @@ __global__ void __launch_bounds__(kAttendThreads, Body::kMinCtas) attend_kernel(
   attend_runs<Body, ROWS>(p, attend_smem);
 }
 
+template <class Body, int ROWS>
+__global__ void __launch_bounds__(kAttendThreads, Body::kMinCtas) attend_item_kernel(const AttendParams p) {
+  extern __shared__ __align__(128) uint8_t attend_smem[];
+  pdl_launch_dependents();
+  pdl_wait();
+  attend_item<Body, ROWS>(p, attend_smem);
+}
+
 // A kernel of the table: how it is launched, what it takes.
 struct AttendKernel {
-  void (*fn)(const AttendParams);
+  void (*fn)(const AttendParams);       // runs of units
+  void (*item_fn)(const AttendParams);  // an item a cluster
   int rows;         // query heads of an item
   int unit;         // slots of a unit
   size_t smem;      // bytes of shared memory
@@ -668,8 +770,8 @@ struct AttendKernel {
 
 template <class Body, int ROWS>
 AttendKernel attend_kernel_of() {
-  return {attend_kernel<Body, ROWS>, ROWS, kWarps * Body::TS,
-          size_t(kWarps) * Body::Feed::kRing + (size_t(ROWS) * Body::kWidth + Body::kBodyFloats) * 4};
+  return {attend_kernel<Body, ROWS>, attend_item_kernel<Body, ROWS>, ROWS, kWarps * Body::TS,
+          size_t(kWarps) * Body::Feed::kRing + (size_t(ROWS) * (2 * Body::kWidth + 2) + Body::kBodyFloats) * 4};
 }
 
 // The kernel for a call of this element type (one translation unit a type).

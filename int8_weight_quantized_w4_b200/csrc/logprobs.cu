@@ -268,20 +268,8 @@ extern "C" w4_status token_logprobs(const float* logits, int64_t ldl, const int3
   // a few thousand logits or more
   unsigned ranks = 1;
   while (ranks < 8 && M * ranks * 2 <= di->sms && V / (ranks * 2) >= 8 * kThreads) ranks *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(M) * ranks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ranks;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  const cudaError_t e = top > 0 ? cudaLaunchKernelEx(&cfg, logprob_kernel<true>, p)
-                                : cudaLaunchKernelEx(&cfg, logprob_kernel<false>, p);
+  const cudaError_t e = launch_pdl(top > 0 ? logprob_kernel<true> : logprob_kernel<false>,
+                                   dim3(static_cast<unsigned>(M) * ranks), kThreads, 0,
+                                   static_cast<cudaStream_t>(stream), ranks, p);
   return e == cudaSuccess ? W4_OK : cuda_fail(e, "launch token_logprobs");
 }

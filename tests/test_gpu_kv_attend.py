@@ -53,26 +53,37 @@ def check(cache, rows_k, rows_v, q, window=0, scale=None, with_acc=False, stride
     return out
 
 
+# Slots that a sequence may grow to: few (an item is a cluster of CTAs) and many
+# (runs of units, joined behind them).
+ROOMS = [0, 20000]
+
+
+def room_for(slots, page):
+    return -(-slots // page) if slots else None
+
+
+@pytest.mark.parametrize("room", ROOMS)
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("heads,group,dim,page", [
     (12, 1, 64, 16), (3, 1, 96, 7), (2, 2, 128, 32), (2, 3, 48, 5), (1, 4, 128, 64), (2, 8, 64, 16), (1, 5, 80, 1),
     (1, 16, 32, 3), (2, 7, 112, 33), (1, 1, 256, 16), (1, 9, 256, 20), (2, 1, 16, 4), (1, 4, 192, 8), (1, 6, 96, 16),
     (1, 2, 160, 16), (1, 12, 128, 16),
 ])
-def test_attend_matches_the_definition(kind, heads, group, dim, page):
+def test_attend_matches_the_definition(kind, heads, group, dim, page, room):
     rng = np.random.default_rng(heads * 1000 + group * 100 + dim + page)
     lengths = [0, 1, 2, 15, 16, 17, 63, 64, 65, 130, 301]
-    cache, k, v = build(rng, kind, lengths, heads, dim, page)
+    cache, k, v = build(rng, kind, lengths, heads, dim, page, max_pages=room_for(room, page))
     q = rng.standard_normal((len(lengths), heads * group, dim)).astype(np.float32)
     check(cache, k, v, q, with_acc=True, strided=True, what=f"{kind} {heads}x{group}x{dim}")
 
 
+@pytest.mark.parametrize("room", ROOMS)
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("window", [1, 5, 64, 100, 5000])
-def test_attend_window(kind, window):
+def test_attend_window(kind, window, room):
     rng = np.random.default_rng(window)
     lengths = [0, 1, 99, 100, 101, 333, 700]
-    cache, k, v = build(rng, kind, lengths, 2, 64, 16)
+    cache, k, v = build(rng, kind, lengths, 2, 64, 16, max_pages=room_for(room, 16))
     q = rng.standard_normal((len(lengths), 4, 64)).astype(np.float32)
     check(cache, k, v, q, window=window, with_acc=True, what=f"window {window}")
 
@@ -87,24 +98,26 @@ def test_attend_one_long_sequence_is_split_and_joined(kind, heads, group, dim, n
     check(cache, k, v, q, with_acc=True, what=f"{kind} {n}")
 
 
+@pytest.mark.parametrize("room", ROOMS)
 @pytest.mark.parametrize("kind", ["float32", "int8"])
-def test_attend_many_sequences(kind):
+def test_attend_many_sequences(kind, room):
     """More sequences than one pass of the run search takes, some empty."""
     rng = np.random.default_rng(17)
     lengths = [int(x) for x in rng.integers(0, 90, 300)]
     lengths[0] = lengths[127] = lengths[128] = lengths[299] = 0
-    cache, k, v = build(rng, kind, lengths, 2, 64, 16)
+    cache, k, v = build(rng, kind, lengths, 2, 64, 16, max_pages=room_for(room, 16))
     q = rng.standard_normal((300, 4, 64)).astype(np.float32)
     check(cache, k, v, q, what="300 sequences")
 
 
+@pytest.mark.parametrize("room", ROOMS)
 @pytest.mark.parametrize("kind", KINDS)
-def test_attend_large_scores_and_values(kind):
+def test_attend_large_scores_and_values(kind, room):
     """Scores of +-100 and more, values of very different magnitude: the
     running maximum rescales, and each rescaling keeps its precision."""
     rng = np.random.default_rng(3)
     for heads, group in ((2, 1), (1, 8)):
-        cache, k, v = build(rng, kind, [257, 64, 1000], heads, 64, 16, amp=6.0)
+        cache, k, v = build(rng, kind, [257, 64, 1000], heads, 64, 16, amp=6.0, max_pages=room_for(room, 16))
         q = (rng.standard_normal((3, heads * group, 64)) * 5).astype(np.float32)
         check(cache, k, v, q, scale=0.3, with_acc=True, what="large scores")
         check(cache, k, v, q, scale=-0.3, what="negative scale")
@@ -168,13 +181,14 @@ def test_attend_offsets_beyond_32_bits():
         check(cache, [rows_k], [rows_v], q, with_acc=True, what="far pages")
 
 
+@pytest.mark.parametrize("room", ROOMS)
 @pytest.mark.parametrize("kind,group", [("float32", 1), ("bfloat16", 4), ("int8", 8), ("float16", 8)])
-def test_attend_nan_reaches_only_its_own_rows(kind, group):
+def test_attend_nan_reaches_only_its_own_rows(kind, group, room):
     """A NaN in q, or Inf and NaN in an attended slot, makes the rows that it
     reaches non-finite and leaves every other row's bits as they were."""
     T = torch()
     rng = np.random.default_rng(41)
-    cache, k, v = build(rng, kind, [150, 90, 33], 2, 64, 16)
+    cache, k, v = build(rng, kind, [150, 90, 33], 2, 64, 16, max_pages=room_for(room, 16))
     q = rng.standard_normal((3, 2 * group, 64)).astype(np.float32)
     base = check(cache, k, v, q, what="clean").cpu().numpy()
     bad = q.copy()
@@ -194,13 +208,14 @@ def test_attend_nan_reaches_only_its_own_rows(kind, group):
     assert np.array_equal(out[0, :group], base[0, :group]) and np.array_equal(out[1:], base[1:])
 
 
-def test_attend_broken_pages_and_lengths_are_recorded():
+@pytest.mark.parametrize("room", ROOMS)
+def test_attend_broken_pages_and_lengths_are_recorded(room):
     """A page id that names no page, and lengths outside the capacity: the
     error word says so, the slots concerned count as empty."""
     T = torch()
     rng = np.random.default_rng(51)
     for kind, group in (("float32", 1), ("bfloat16", 4), ("int8", 8)):
-        cache, k, v = build(rng, kind, [40, 48], 2, 64, 16)
+        cache, k, v = build(rng, kind, [40, 48], 2, 64, 16, max_pages=room_for(room, 16))
         q = rng.standard_normal((2, 2 * group, 64)).astype(np.float32)
         qd = T.from_numpy(q).cuda()
         clear_error()
@@ -213,7 +228,8 @@ def test_attend_broken_pages_and_lengths_are_recorded():
             ro, _, _, (to, _, _) = oracle.kv_attend_ref(q[0], k[0][j], v[0][j], 0.125)
             assert np.all(np.abs(out[0] - ro) <= to)
         cache.page_table[0, 1] = good
-        cache.lengths.copy_(T.tensor([-5, 49], dtype=T.int32))
+        # entries behind the last page name none: a length beyond the capacity ends there
+        cache.lengths.copy_(T.tensor([-5, cache.capacity + 1], dtype=T.int32))
         out = w4().kv_attend(qd, cache).cpu().double().numpy()
         assert error_status() == 8
         assert np.all(out[0] == 0)
@@ -221,14 +237,15 @@ def test_attend_broken_pages_and_lengths_are_recorded():
         assert np.all(np.abs(out[1] - ro) <= to)
 
 
+@pytest.mark.parametrize("room", ROOMS)
 @pytest.mark.parametrize("kind,group", [("float32", 1), ("float16", 4)])
-def test_attend_in_a_graph_follows_the_lengths(kind, group):
+def test_attend_in_a_graph_follows_the_lengths(kind, group, room):
     """A captured call is replayed while the lengths change, two captured
     calls are replayed on two streams at once, and every result is bit for bit
     what an eager call gives."""
     T = torch()
     rng = np.random.default_rng(61)
-    cache, k, v = build(rng, kind, [500, 3, 260], 2, 64, 16)
+    cache, k, v = build(rng, kind, [500, 3, 260], 2, 64, 16, max_pages=room_for(room, 16))
     q = T.from_numpy(rng.standard_normal((3, 2 * group, 64)).astype(np.float32)).cuda()
     q2 = T.from_numpy(rng.standard_normal((3, 2 * group, 64)).astype(np.float32)).cuda()
     w4().kv_attend(q, cache)
@@ -293,7 +310,7 @@ def test_attend_refusals():
     with pytest.raises(w4().W4Error):
         w4().kv_attend(q, cache, scale=float("nan"))
     with pytest.raises(w4().W4Error) as e:
-        w4().kv_attend(q, cache, ws=T.empty(16, dtype=T.uint8, device="cuda"))
+        w4().kv_attend(q, cache, acc=T.zeros((2, 48), device="cuda"), ws=T.empty(16, dtype=T.uint8, device="cuda"))
     assert e.value.status == 7
     with pytest.raises(ValueError):
         w4().kv_attend(q, cache, lse=T.zeros((2, 2), device="cuda"))

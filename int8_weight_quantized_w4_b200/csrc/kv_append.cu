@@ -281,14 +281,14 @@ extern "C" w4_status kv_append(const kv_cache* c, const float* k, int64_t ldk, c
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (c->type) {
-    case W4_KV_F32: e = launch_pdl(append_kernel<W4_KV_F32>, grid, kThreads, 0, st, 1, p); break;
-    case W4_KV_F16: e = launch_pdl(append_kernel<W4_KV_F16>, grid, kThreads, 0, st, 1, p); break;
-    case W4_KV_BF16: e = launch_pdl(append_kernel<W4_KV_BF16>, grid, kThreads, 0, st, 1, p); break;
-    default: e = launch_pdl(append_kernel<W4_KV_I8>, grid, kThreads, 0, st, 1, p); break;
+    case W4_KV_F32: e = launch_pdl(append_kernel<W4_KV_F32>, grid, kThreads, 0, st, 1, false, p); break;
+    case W4_KV_F16: e = launch_pdl(append_kernel<W4_KV_F16>, grid, kThreads, 0, st, 1, false, p); break;
+    case W4_KV_BF16: e = launch_pdl(append_kernel<W4_KV_BF16>, grid, kThreads, 0, st, 1, false, p); break;
+    default: e = launch_pdl(append_kernel<W4_KV_I8>, grid, kThreads, 0, st, 1, false, p); break;
   }
   if (e != cudaSuccess) return cuda_fail(e, "launch kv_append");
   if (in_place) {
-    e = launch_pdl(advance_kernel, dim3(static_cast<unsigned>(by_seq)), kThreads, 0, st, 1, p, lengths_out);
+    e = launch_pdl(advance_kernel, dim3(static_cast<unsigned>(by_seq)), kThreads, 0, st, 1, false, p, lengths_out);
     if (e != cudaSuccess) return cuda_fail(e, "launch kv_append (lengths)");
   }
   return W4_OK;

@@ -25,11 +25,16 @@ constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kMostUnits = 4;
 constexpr int kMaxLaneVecs = 2;  // float4s of a lane: 32 x 4 x 2 = 256, the largest head_dim
 
+// The kernels behind the attention kernel do not let the next one begin early,
+// and ask for the attention's split of shared memory: a CTA of theirs that
+// lies between those of the next call's attention leaves room for one less on
+// its SM for as long as that runs (131072 slots of 8 x 128 bf16, call after
+// call: 117 us with either, 95 us without).
+//
 // One query head per `wpr` warps: wpr = 8 spreads the partials of a few long
 // rows, wpr = 1 passes over many rows that mostly have nothing to join.
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p, int wpr) {
   __shared__ Triple sm[kJoinWarps][32 * kMaxLaneVecs];
-  pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int q_heads = p.c.heads * p.group;
@@ -75,23 +80,36 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
     if (lane + 32 * j < vecs) write_out(p, b, qh, 4 * (lane + 32 * j), x[j]);
 }
 
-// acc[b, j] += sum over the query heads of 2^(x - lse2), heads in order.
+// acc[b, j] += sum over the query heads of 2^(x - lse2). A warp takes 32 slots
+// and every 8th head; the warps' sums are added in their order.
 __global__ void __launch_bounds__(kJoinThreads) gather_kernel(const AttendParams p, float* acc, int64_t ldacc) {
-  pdl_launch_dependents();
+  __shared__ float sums[kJoinWarps][32];
   pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t b = blockIdx.y;
   const int q_heads = p.c.heads * p.group;
   int32_t lo, n;
   attended(p, b, lo, n);
   const float* z = p.lse2 + int64_t(b) * q_heads;
-  for (int64_t j = lo + int64_t(blockIdx.x) * kJoinThreads + threadIdx.x; j < n; j += int64_t(gridDim.x) * kJoinThreads) {
+  for (int64_t j0 = lo + int64_t(blockIdx.x) * 32; j0 < n; j0 += int64_t(gridDim.x) * 32) {
+    const int64_t j = j0 + lane;
     const float* x = p.scores + int64_t(b) * q_heads * p.c.capacity + j;
     float sum = 0.f;
-    for (int i = 0; i < q_heads; ++i) {
-      const float zi = z[i];  // -Inf: every attended score is -Inf, and weighs nothing
-      sum += zi == -INFINITY ? 0.f : ex2(x[int64_t(i) * p.c.capacity] - zi);
+    if (j < n) {
+#pragma unroll 4
+      for (int i = warp; i < q_heads; i += kJoinWarps) {
+        const float zi = z[i];  // -Inf: every attended score is -Inf, and weighs nothing
+        sum += zi == -INFINITY ? 0.f : ex2(x[int64_t(i) * p.c.capacity] - zi);
+      }
     }
-    acc[int64_t(b) * ldacc + j] += sum;
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && j < n) {
+#pragma unroll
+      for (int w = 1; w < kJoinWarps; ++w) sum += sums[w][lane];
+      acc[int64_t(b) * ldacc + j] += sum;
+    }
+    __syncthreads();
   }
 }
 
@@ -254,21 +272,21 @@ extern "C" w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, i
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (L.ranks != 0) {
-    e = launch_pdl(L.kernel.item_fn, dim3(L.ctas), kAttendThreads, L.kernel.smem, st, L.ranks, p);
+    e = launch_pdl(L.kernel.item_fn, dim3(L.ctas), kAttendThreads, L.kernel.smem, st, L.ranks, true, p);
   } else {
-    e = launch_pdl(L.kernel.fn, dim3(L.ctas), kAttendThreads, L.kernel.smem, st, 1, p);
+    e = launch_pdl(L.kernel.fn, dim3(L.ctas), kAttendThreads, L.kernel.smem, st, 1, true, p);
     if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend");
     const int64_t rows = c->seqs * q_heads;
     const int wpr = rows <= int64_t(di->sms) * kJoinWarps ? kJoinWarps : 1;
     const int64_t rows_per_cta = kJoinWarps / wpr;
     e = launch_pdl(join_kernel, dim3(static_cast<unsigned>((rows + rows_per_cta - 1) / rows_per_cta)), kJoinThreads, 0,
-                   st, 1, p, wpr);
+                   st, 1, true, p, wpr);
   }
   if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend");
   if (acc != nullptr && p.c.capacity > 0) {
-    const int64_t per_row = (p.c.capacity + kJoinThreads - 1) / kJoinThreads;
-    const dim3 grid(static_cast<unsigned>(per_row < 512 ? per_row : 512), static_cast<unsigned>(c->seqs));
-    e = launch_pdl(gather_kernel, grid, kJoinThreads, 0, st, 1, p, acc, ldacc);
+    const int64_t per_row = (p.c.capacity + 31) / 32;
+    const dim3 grid(static_cast<unsigned>(per_row < 1024 ? per_row : 1024), static_cast<unsigned>(c->seqs));
+    e = launch_pdl(gather_kernel, grid, kJoinThreads, 0, st, 1, true, p, acc, ldacc);
     if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend (weights)");
   }
   return W4_OK;

@@ -351,7 +351,7 @@ extern "C" w4_status kv_evict(const kv_cache* src, const float* acc, int64_t lda
   // SMs and a CTA's share is a few thousand slots or more
   unsigned ranks = 1;
   while (ranks < 8 && src->seqs * ranks * 2 <= di->sms && p.c.capacity / (ranks * 2) >= 2 * kSelThreads) ranks *= 2;
-  cudaError_t e = launch_pdl(select_kernel, dim3(static_cast<unsigned>(src->seqs) * ranks), kSelThreads, 0, st, ranks, p);
+  cudaError_t e = launch_pdl(select_kernel, dim3(static_cast<unsigned>(src->seqs) * ranks), kSelThreads, 0, st, ranks, false, p);
   if (e != cudaSuccess) return cuda_fail(e, "launch kv_evict (select)");
   const int elem = elem_bytes(src->type), vecs = src->head_dim * elem / 16;
   const int64_t most = width < p.d.capacity ? width : p.d.capacity;
@@ -359,11 +359,11 @@ extern "C" w4_status kv_evict(const kv_cache* src, const float* acc, int64_t lda
   if (in_place) {
     const int per = vecs < 4 ? vecs : 4;
     const dim3 grid((vecs + per - 1) / per, 2 * src->kv_heads, static_cast<unsigned>(src->seqs));
-    e = launch_pdl(move_kernel<true>, grid, kMoveThreads, 0, st, 1, p, vecs, per, elem);
+    e = launch_pdl(move_kernel<true>, grid, kMoveThreads, 0, st, 1, false, p, vecs, per, elem);
   } else {
     const int rows = kMoveThreads / vecs * kMoveUnroll;
     const dim3 grid(static_cast<unsigned>((most + rows - 1) / rows), 2 * src->kv_heads, static_cast<unsigned>(src->seqs));
-    e = launch_pdl(move_kernel<false>, grid, kMoveThreads, 0, st, 1, p, vecs, vecs, elem);
+    e = launch_pdl(move_kernel<false>, grid, kMoveThreads, 0, st, 1, false, p, vecs, vecs, elem);
   }
   return e == cudaSuccess ? W4_OK : cuda_fail(e, "launch kv_evict (move)");
 }

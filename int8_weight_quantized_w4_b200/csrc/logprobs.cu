@@ -270,6 +270,6 @@ extern "C" w4_status token_logprobs(const float* logits, int64_t ldl, const int3
   while (ranks < 8 && M * ranks * 2 <= di->sms && V / (ranks * 2) >= 8 * kThreads) ranks *= 2;
   const cudaError_t e = launch_pdl(top > 0 ? logprob_kernel<true> : logprob_kernel<false>,
                                    dim3(static_cast<unsigned>(M) * ranks), kThreads, 0,
-                                   static_cast<cudaStream_t>(stream), ranks, p);
+                                   static_cast<cudaStream_t>(stream), ranks, false, p);
   return e == cudaSuccess ? W4_OK : cuda_fail(e, "launch token_logprobs");
 }

@@ -4,11 +4,18 @@
 // Bound by its bytes (fp32 rows in, stored rows out) for prompts and by
 // latency for a decode step. A token is one CTA, so that its place in the
 // cache (a search in cu_tokens, the length, the page: three dependent reads)
-// is found once; its 2 x heads rows of head_dim go to half-warps, 16 lanes of
-// 4 elements wide, which is what a row's maximum (int8) is reduced over.
+// is found once, while the token's first 32 KB are already on their way. int8
+// rows go to half-warps, 16 lanes of 4 elements wide, which a row's maximum is
+// reduced over; the others are copied as they come, 4 elements a thread.
 #include "kv_cache.cuh"
 
 namespace w4host {
+
+w4kv::Divisor divisor(uint32_t d) {
+  uint32_t l = 0;
+  while ((1u << l) < d) ++l;
+  return {d, static_cast<uint32_t>(((uint64_t((1u << l) - d) << 32) / d) + 1), l};
+}
 
 w4_status check_cache(const kv_cache* c, const char* what, w4kv::View* out) {
   if (c == nullptr) return fail(W4_ERR_NULL, "%s is NULL", what);
@@ -55,10 +62,7 @@ w4_status check_cache(const kv_cache* c, const char* what, w4kv::View* out) {
   out->heads = c->kv_heads;
   out->slots_per_page = c->page_size;
   out->page_rows = static_cast<uint32_t>(c->page_stride / c->head_dim);
-  const uint32_t d = static_cast<uint32_t>(c->page_size);
-  uint32_t l = 0;
-  while ((1u << l) < d) ++l;
-  out->page = {d, static_cast<uint32_t>(((uint64_t((1u << l) - d) << 32) / d) + 1), l};
+  out->page = divisor(static_cast<uint32_t>(c->page_size));
   out->dim = c->head_dim;
   out->capacity = static_cast<int32_t>(c->max_pages * c->page_size);
   return W4_OK;
@@ -83,6 +87,7 @@ struct AppendParams {
   int64_t tokens;
   int32_t* lengths_out;  // NULL: written by advance_kernel
   int32_t vec;           // both inputs' rows are 16-byte aligned
+  Divisor quads;         // float4s of a row of head_dim elements
   ErrorWord* err;
 };
 
@@ -117,7 +122,7 @@ __device__ int32_t sequence_of(const AppendParams& p, int64_t t) {
 }
 
 template <int TYPE>
-__device__ __forceinline__ void store4(void* dst, int64_t at, float4 x, double s) {
+__device__ __forceinline__ void store4(void* dst, int64_t at, float4 x) {
   if constexpr (TYPE == W4_KV_F32) {
     reinterpret_cast<float4*>(dst)[at / 4] = x;
   } else if constexpr (TYPE == W4_KV_F16) {
@@ -126,33 +131,121 @@ __device__ __forceinline__ void store4(void* dst, int64_t at, float4 x, double s
     w.x = *reinterpret_cast<const uint32_t*>(&a);
     w.y = *reinterpret_cast<const uint32_t*>(&b);
     reinterpret_cast<uint2*>(dst)[at / 4] = w;
-  } else if constexpr (TYPE == W4_KV_BF16) {
+  } else {
     const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
     uint2 w;
     w.x = *reinterpret_cast<const uint32_t*>(&a);
     w.y = *reinterpret_cast<const uint32_t*>(&b);
     reinterpret_cast<uint2*>(dst)[at / 4] = w;
-  } else {
-    // the quotient in fp64, as the definition has it: an fp32 quotient rounds
-    // some values onto a half and then to another code
-    const auto code = [s](float f) {
-      const double q = rint(static_cast<double>(f) / s);
-      return static_cast<uint32_t>(static_cast<int>(fmin(fmax(q, -127.0), 127.0))) & 0xFFu;
-    };
-    reinterpret_cast<uint32_t*>(dst)[at / 4] = code(x.x) | code(x.y) << 8 | code(x.z) << 16 | code(x.w) << 24;
   }
 }
 
+__device__ __forceinline__ float4 load4(const AppendParams& p, const float* src) {
+  return p.vec ? __ldg(reinterpret_cast<const float4*>(src)) : make_float4(src[0], src[1], src[2], src[3]);
+}
+
+// Rows without a scale: float4 i of the token's keys, then of its values.
+template <int TYPE>
+struct Copied {
+  static constexpr int kAhead = 8;
+  float4 x[kAhead];
+
+  __device__ __forceinline__ void load(const AppendParams& p, int64_t t, int32_t from) {
+    const int32_t half = p.c.heads * p.c.dim / 4;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int32_t i = from + threadIdx.x + j * kThreads;
+      if (i < half) x[j] = load4(p, p.k + t * p.ldk + 4 * i);
+      else if (i < 2 * half) x[j] = load4(p, p.v + t * p.ldv + 4 * (i - half));
+    }
+  }
+  // page_at: elements to the page; inner: the slot in it
+  __device__ __forceinline__ void store(const AppendParams& p, int64_t page_at, int32_t inner, int32_t from) const {
+    const int32_t half = p.c.heads * p.c.dim / 4;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int32_t i = from + threadIdx.x + j * kThreads;
+      if (i < 2 * half) {
+        const int32_t r = i < half ? i : i - half, h = p.quads.quotient(r), d = r - h * (p.c.dim / 4);
+        const int64_t at = page_at + (int64_t(h) * p.c.slots_per_page + inner) * p.c.dim + 4 * d;
+        store4<TYPE>(i < half ? p.c.k : p.c.v, at, x[j]);
+      }
+    }
+  }
+};
+
+// int8: a row of head_dim elements for each 16 lanes, keys' rows, then values'.
+struct Quantised {
+  float4 x[kRowVecs];
+
+  __device__ __forceinline__ void load(const AppendParams& p, int64_t t, int32_t from) {
+    const int lane = threadIdx.x % kRowLanes;
+    const int32_t r = from + threadIdx.x / kRowLanes;
+    const float* src = r < p.c.heads ? p.k + t * p.ldk + int64_t(r) * p.c.dim : p.v + t * p.ldv + int64_t(r - p.c.heads) * p.c.dim;
+#pragma unroll
+    for (int i = 0; i < kRowVecs; ++i) {
+      const int at = lane + i * kRowLanes;
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < 2 * p.c.heads && at < p.c.dim / 4) x[i] = load4(p, src + 4 * at);
+    }
+  }
+  __device__ __forceinline__ void store(const AppendParams& p, int32_t page, int32_t inner, int32_t from) {
+    const View& c = p.c;
+    const int lane = threadIdx.x % kRowLanes;
+    const int32_t r = from + threadIdx.x / kRowLanes;
+    const bool live = r < 2 * c.heads, is_v = r >= c.heads;
+    const int32_t h = is_v ? r - c.heads : r;
+    float top = 0.f, poison = 0.f;  // NaN for an Inf or NaN in the row
+#pragma unroll
+    for (int i = 0; i < kRowVecs; ++i) {
+      top = fmaxf(fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y))), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
+      poison += x[i].x * 0.f + x[i].y * 0.f + (x[i].z * 0.f + x[i].w * 0.f);
+    }
+#pragma unroll
+    for (int o = kRowLanes / 2; o > 0; o /= 2) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      poison += __shfl_xor_sync(0xffffffffu, poison, o);
+    }
+    // the fp64 quotient rounded to fp32 is the correctly rounded fp32 one
+    const bool bad = poison != 0.f;
+    const float sc = bad ? __int_as_float(0x7fc00000) : (top > 0.f ? __fdiv_rn(top, 127.f) : 1.f);
+    // a scale that underflows to 0 stores zeros, which it also stands for
+    const double s = bad || sc == 0.f ? static_cast<double>(INFINITY) : static_cast<double>(sc);
+    if (!live) return;
+    const int64_t row = int64_t(h) * c.slots_per_page + inner;
+    if (lane == 0) (is_v ? c.vs : c.ks)[int64_t(page) * c.heads * c.slots_per_page + row] = sc;
+    uint8_t* base = static_cast<uint8_t*>(is_v ? c.v : c.k) + int64_t(page) * c.page_stride + row * c.dim;
+#pragma unroll
+    for (int i = 0; i < kRowVecs; ++i) {
+      const int at = lane + i * kRowLanes;
+      if (at < c.dim / 4)
+        reinterpret_cast<uint32_t*>(base)[at] =
+            bad ? 0u : code(x[i].x, s) | code(x[i].y, s) << 8 | code(x[i].z, s) << 16 | code(x[i].w, s) << 24;
+    }
+  }
+  // The quotient in fp64, as the definition has it: an fp32 quotient rounds
+  // some values onto a half and then to another code.
+  __device__ static __forceinline__ uint32_t code(float f, double s) {
+    const double q = rint(static_cast<double>(f) / s);
+    return static_cast<uint32_t>(static_cast<int>(fmin(fmax(q, -127.0), 127.0))) & 0xFFu;
+  }
+};
+
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+  constexpr bool I8 = TYPE == W4_KV_I8;
   pdl_launch_dependents();
   pdl_wait();
   const View& c = p.c;
+  typename std::conditional<I8, Quantised, Copied<TYPE>>::type data;
+  const int32_t step = I8 ? kThreads / kRowLanes : Copied<TYPE>::kAhead * kThreads;
+  const int32_t count = I8 ? 2 * c.heads : 2 * c.heads * c.dim / 4;
+  const int64_t t = blockIdx.x;
+  if (t < p.tokens) data.load(p, t, 0);
   // the new lengths, where they go to memory of their own
   const int64_t b_of_thread = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   if (p.lengths_out != nullptr && p.cu != nullptr && b_of_thread < c.seqs)
     p.lengths_out[b_of_thread] = advanced(p, static_cast<int32_t>(b_of_thread));
-  const int64_t t = blockIdx.x;
   if (t >= p.tokens) return;
   int32_t b = static_cast<int32_t>(t), slot;
   if (p.cu == nullptr) {
@@ -171,60 +264,16 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     if (threadIdx.x == 0) w4dev::record_error(p.err, W4_ERR_VALUE, w4dev::K_KV_APPEND, b);
     return;
   }
-  const int32_t page = page_of(c, b, c.page.quotient(slot), p.err, w4dev::K_KV_APPEND);
+  const int32_t index = c.page.quotient(slot);
+  const int32_t page = page_of(c, b, index, p.err, w4dev::K_KV_APPEND);
   if (page < 0) return;
-  const int32_t inner = slot % c.slots_per_page;
-  const int lane = threadIdx.x % kRowLanes;
-  const int vecs = c.dim / 4;
-  for (int32_t r0 = 0; r0 < 2 * c.heads; r0 += kThreads / kRowLanes) {
-    const int32_t r = r0 + threadIdx.x / kRowLanes;
-    const bool live = r < 2 * c.heads;
-    const bool is_v = r >= c.heads;
-    const int32_t h = is_v ? r - c.heads : r;
-    const float* src = (is_v ? p.v + t * p.ldv : p.k + t * p.ldk) + int64_t(live ? h : 0) * c.dim;
-    float4 x[kRowVecs];
-    float top = 0.f, poison = 0.f;
-#pragma unroll
-    for (int i = 0; i < kRowVecs; ++i) {
-      const int at = lane + i * kRowLanes;
-      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (live && at < vecs) {
-        if (p.vec) {
-          x[i] = *reinterpret_cast<const float4*>(src + 4 * at);
-        } else {
-          x[i] = make_float4(src[4 * at], src[4 * at + 1], src[4 * at + 2], src[4 * at + 3]);
-        }
-      }
-      if constexpr (TYPE == W4_KV_I8) {
-        top = fmaxf(fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y))), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
-        poison += x[i].x * 0.f + x[i].y * 0.f + (x[i].z * 0.f + x[i].w * 0.f);  // NaN for an Inf or NaN
-      }
-    }
-    const int64_t row = (int64_t(h) * c.slots_per_page + inner);
-    double s = 1.0;
-    if constexpr (TYPE == W4_KV_I8) {
-#pragma unroll
-      for (int o = kRowLanes / 2; o > 0; o /= 2) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        poison += __shfl_xor_sync(0xffffffffu, poison, o);
-      }
-      // the fp64 quotient rounded to fp32 is the correctly rounded fp32 one
-      const float sc = poison != 0.f ? __int_as_float(0x7fc00000) : (top > 0.f ? __fdiv_rn(top, 127.f) : 1.f);
-      // a scale that underflows to 0 stores zeros, which it also stands for
-      s = (poison != 0.f || sc == 0.f) ? static_cast<double>(INFINITY) : static_cast<double>(sc);
-      if (poison != 0.f) {
-#pragma unroll
-        for (int i = 0; i < kRowVecs; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      if (live && lane == 0)
-        (is_v ? c.vs : c.ks)[int64_t(page) * c.heads * c.slots_per_page + row] = sc;
-    }
-    if (!live) continue;
-    uint8_t* base = static_cast<uint8_t*>(is_v ? c.v : c.k) + int64_t(page) * c.page_stride * Elem<TYPE>::kBytes;
-#pragma unroll
-    for (int i = 0; i < kRowVecs; ++i) {
-      const int at = lane + i * kRowLanes;
-      if (at < vecs) store4<TYPE>(base, row * c.dim + 4 * at, x[i], s);
+  const int32_t inner = slot - index * c.slots_per_page;
+  for (int32_t from = 0; from < count; from += step) {
+    if (from > 0) data.load(p, t, from);
+    if constexpr (I8) {
+      data.store(p, page, inner, from);
+    } else {
+      data.store(p, int64_t(page) * c.page_stride, inner, from);
     }
   }
 }
@@ -273,6 +322,7 @@ extern "C" w4_status kv_append(const kv_cache* c, const float* k, int64_t ldk, c
   p.cu = cu_tokens;
   p.tokens = tokens;
   p.err = di->err;
+  p.quads = divisor(static_cast<uint32_t>(c->head_dim) / 4);
   p.vec = ((bits(k) | bits(v)) & 15) == 0 && (tokens <= 1 || ((ldk | ldv) & 3) == 0);
   const bool in_place = cu_tokens != nullptr && lengths_out == c->lengths;
   p.lengths_out = in_place ? nullptr : lengths_out;

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "w4_device.cuh"
 #include "w4_internal.h"
@@ -132,6 +133,8 @@ __device__ __forceinline__ float ex2(float x) {
 }  // namespace w4kv
 
 namespace w4host {
+
+w4kv::Divisor divisor(uint32_t d);
 
 // Checks of a cache descriptor that need no device, and the kernels' view of
 // it. `what` names the descriptor in the reason.

@@ -8,11 +8,13 @@
 // ties need no rule of their own.
 //
 // Work. A row is one cluster of CTAs, as many as fill the SMs when there are
-// few rows; its parts meet in the first one's shared memory. Each warp keeps
-// its best 32 keys sorted, one a lane: a logit below the last of the wanted
-// ones is dropped by one comparison, and of n unordered logits only about
-// top * ln(n / top) pass it. Bound by reading the logits, by latency where
-// there are few rows.
+// few rows; its parts meet in the first one's shared memory. A thread takes 16
+// logits at a time: their maximum decides both whether the sums have to be
+// rescaled and whether any of them can be an alternative. Each warp keeps its
+// best 32 keys sorted, one a lane, and drops what lies below the last wanted
+// one of any warp of the CTA (of n unordered logits about top * ln(n / top)
+// pass); to begin with, the top-th largest of the 32 lanes' first maxima is
+// such a bound. Bound by reading the logits, by latency where there are few.
 #include <cooperative_groups.h>
 
 #include "kv_cache.cuh"
@@ -75,16 +77,20 @@ __device__ __forceinline__ void join(Sums& a, Sums b) {
   a.m = m;
 }
 
-__device__ __forceinline__ void add(Sums& s, float x) {
-  if (x > s.m) {
-    if (s.m != -INFINITY) shift(s.l, s.t, s.m - x);
-    s.m = x;
+// N logits of which `top` is the largest (NaN aside).
+template <int N>
+__device__ __forceinline__ void add(Sums& s, const float (&x)[N], float top) {
+  if (top > s.m) {
+    if (s.m != -INFINITY) shift(s.l, s.t, s.m - top);
+    s.m = top;
   }
-  if (x != -INFINITY) {  // NaN goes on: it makes l NaN
-    const float d = x - s.m;
-    const float e = ex2(d * kLog2e);
+  const float ref = s.m == -INFINITY ? 0.f : s.m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float d = x[i] - ref;
+    const float e = ex2(d * kLog2e);  // NaN goes on: it makes l NaN
     s.l += e;
-    s.t = e > 0.f ? fmaf(e, d, s.t) : s.t;  // d may be -Inf where e is 0
+    s.t = fmaf(e, fmaxf(d, -1e30f), s.t);  // d may be -Inf, where e is 0
   }
 }
 
@@ -114,12 +120,26 @@ __device__ __forceinline__ Key merge(Key a, Key b, int lane) {
   return x;
 }
 
+// The lanes' keys sorted, the largest in lane 0.
+__device__ __forceinline__ Key sort(Key x, int lane) {
+#pragma unroll
+  for (int k = 2; k <= 32; k *= 2)
+#pragma unroll
+    for (int o = k / 2; o > 0; o /= 2) {
+      const Key y = __shfl_xor_sync(0xffffffffu, x, o);
+      const bool larger = ((lane & o) == 0) == ((lane & k) == 0 || k == 32);
+      x = larger ? (x > y ? x : y) : (x < y ? x : y);
+    }
+  return x;
+}
+
 template <bool TOP>
-__global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParams p) {
   __shared__ Sums sm_sums[kWarpsLp];
   __shared__ Key sm_keys[TOP ? kWarpsLp : 1][32];
   __shared__ Sums cta_sums;
   __shared__ Key cta_keys[32];
+  __shared__ Key cta_bar;
   pdl_launch_dependents();
   pdl_wait();
   cg::cluster_group cluster = cg::this_cluster();
@@ -137,57 +157,89 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobParams p
 
   Sums s = {-INFINITY, 0.f, 0.f};
   Key list = 0;
-  Key bar = 0;  // the last wanted key of the warp's list, and its logit
+  Key bar = 0;  // a bound that the wanted keys of the CTA's part do not lie below, and its logit
   float bar_x = -INFINITY;
-  const auto offer = [&](float v, int32_t id, bool there) {
-    const bool maybe = there && !(v < bar_x);
-    if (__any_sync(0xffffffffu, maybe)) {
-      const Key k = maybe ? logit_key(v, static_cast<uint32_t>(id)) : 0;
-      insert(list, k, maybe && k > bar, lane);
-      bar = shfl_key(list, p.top - 1);
+  if (TOP && tid == 0) cta_bar = 0;
+  const auto raise = [&](Key k) {
+    if (k > bar) {
+      bar = k;
       const float b = key_logit(bar);
       bar_x = b == b ? b : -INFINITY;
     }
   };
-  if (warp == 0) {
+  const auto offer = [&](float v, int32_t id, bool there) {
+    const bool maybe = there && !(v < bar_x);
+    if (__any_sync(0xffffffffu, maybe)) {
+      const Key k = maybe ? logit_key(v, static_cast<uint32_t>(id)) : 0;
+      insert(list, k, maybe && k >= bar, lane);
+    }
+  };
+  constexpr int kQuads = 4;  // float4s of a thread at a time
+  int32_t q = q0 + warp * 32;
+  float4 v[kQuads];
+  const auto load = [&](int32_t from) {
+#pragma unroll
+    for (int u = 0; u < kQuads; ++u) {
+      const int32_t at = from + u * kThreads + lane;
+      v[u] = at < q1 ? __ldg(xq + at) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    }
+  };
+  if (q < q1) load(q);
+  if (TOP) __syncthreads();  // cta_bar is 0
+  if (warp == kWarpsLp - 1) {
     const int32_t tail = lead + 4 * quads;
     if (rank == 0 && lead > 0) {
       const bool there = lane < lead;
-      const float v = there ? x[lane] : -INFINITY;
-      if (there) add(s, v);
-      if (TOP) offer(v, lane, there);
+      const float w[1] = {there ? x[lane] : -INFINITY};
+      add(s, w, w[0]);
+      if (TOP) offer(w[0], lane, there);
     }
     if (rank == ranks - 1 && tail < p.V) {
       const bool there = tail + lane < p.V;
-      const float v = there ? x[tail + lane] : -INFINITY;
-      if (there) add(s, v);
-      if (TOP) offer(v, tail + lane, there);
+      const float w[1] = {there ? x[tail + lane] : -INFINITY};
+      add(s, w, w[0]);
+      if (TOP) offer(w[0], tail + lane, there);
     }
   }
-  constexpr int kAhead = 4;
-  for (int32_t q = q0 + warp * 32; q < q1; q += kAhead * kThreads) {
-    float4 v[kAhead];
+  bool begun = false;
+  for (; q < q1; q += kQuads * kThreads) {
+    float w[4 * kQuads];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int32_t at = q + u * kThreads + lane;
-      v[u] = at < q1 ? __ldg(xq + at) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    for (int u = 0; u < kQuads; ++u) {
+      w[4 * u] = v[u].x;
+      w[4 * u + 1] = v[u].y;
+      w[4 * u + 2] = v[u].z;
+      w[4 * u + 3] = v[u].w;
     }
+    const int32_t next = q + kQuads * kThreads;
+    if (next < q1) load(next);
+    float top = w[0];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int32_t at = q + u * kThreads + lane;
-      add(s, v[u].x);
-      add(s, v[u].y);
-      add(s, v[u].z);
-      add(s, v[u].w);
-      if (TOP) {
-        const bool there = at < q1;
-        const bool maybe = there && !(v[u].x < bar_x && v[u].y < bar_x && v[u].z < bar_x && v[u].w < bar_x);
-        if (__any_sync(0xffffffffu, maybe)) {
+    for (int i = 1; i < 4 * kQuads; ++i) top = fmaxf(top, w[i]);
+    add(s, w, top);
+    if (TOP) {
+      if (!begun) {
+        // a lane's maximum is a logit of its own (unless it is -Inf or NaN): `top` of them lie at or above the top-th
+        begun = true;
+        const Key k = top > -INFINITY ? logit_key(top, 0xFFFFFFFFu) : 0;
+        raise(shfl_key(sort(k, lane), p.top - 1));
+        if (lane == 0 && bar != 0) atomicMax(&cta_bar, bar);
+      }
+      // NaN is never the maximum, and only matters where fewer than `top` others are there
+      if (__any_sync(0xffffffffu, !(top < bar_x))) {
+        raise(*static_cast<volatile Key*>(&cta_bar));
+#pragma unroll
+        for (int u = 0; u < kQuads; ++u) {
+          const int32_t at = q + u * kThreads + lane;
+          const bool there = at < q1;
           const int32_t id = lead + 4 * at;
-          offer(v[u].x, id, there);
-          offer(v[u].y, id + 1, there);
-          offer(v[u].z, id + 2, there);
-          offer(v[u].w, id + 3, there);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) offer(w[4 * u + e], id + e, there);
+        }
+        const Key last = shfl_key(list, p.top - 1);
+        if (last > bar) {
+          raise(last);
+          if (lane == 0) atomicMax(&cta_bar, last);
         }
       }
     }
@@ -264,10 +316,10 @@ extern "C" w4_status token_logprobs(const float* logits, int64_t ldl, const int3
   const w4_status rc = current_device(&di);
   if (rc != W4_OK) return rc;
   const LogprobParams p = {logits, ldl, tokens, static_cast<int32_t>(V), top, logp, entropy, top_logp, top_ids, di->err};
-  // CTAs of a row: up to 8, while the rows alone leave SMs idle and a CTA has
-  // a few thousand logits or more
+  // CTAs of a row: up to 8, while the rows alone do not give every SM four and
+  // a CTA has a few thousand logits or more
   unsigned ranks = 1;
-  while (ranks < 8 && M * ranks * 2 <= di->sms && V / (ranks * 2) >= 8 * kThreads) ranks *= 2;
+  while (ranks < 8 && M * ranks * 2 <= 4 * di->sms && V / (ranks * 2) >= 8 * kThreads) ranks *= 2;
   const cudaError_t e = launch_pdl(top > 0 ? logprob_kernel<true> : logprob_kernel<false>,
                                    dim3(static_cast<unsigned>(M) * ranks), kThreads, 0,
                                    static_cast<cudaStream_t>(stream), ranks, false, p);

@@ -742,7 +742,9 @@ def kv_evict(cache: KvCache, acc, keep: int, recent: int = 0, dst: KvCache | Non
     ld = _matrix(acc, "acc", torch.float32, B, cache.capacity, dev)
     ldo = _matrix(acc_out, "acc_out", torch.float32, B, cache.capacity, dev)
     ldk = 0 if kept is None else _matrix(kept, "kept", torch.int32, B, keep, dev)
-    need = int(lib().kv_evict_workspace_size(cache._ref, keep))
+    need = cache._need.get(keep)
+    if need is None:
+        need = cache._need[keep] = int(lib().kv_evict_workspace_size(cache._ref, keep))
     if ws is None and need:
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     st = lib().kv_evict(cache._ref, acc.data_ptr(), ld, keep, recent, dst._ref, acc_out.data_ptr(), ldo, _ptr(kept),

@@ -4,9 +4,10 @@
 // slot that stays, is found exactly by four passes over 8-bit digits of an
 // order-preserving key (a histogram a pass, in shared memory, added up over
 // the cluster's CTAs); ties at the threshold stay from the lowest slot on. A
-// CTA reads its weights once and keeps their keys in shared memory, up to
-// 16384 of them. Then each thread places four neighbouring slots behind the
-// kept ones before them: the kept slots' list.
+// CTA reads its weights once and keeps them in shared memory, up to 16384; each
+// warp looks for the digit by itself, so that a pass has one barrier. Then each
+// thread places four neighbouring slots behind the kept ones before them: the
+// kept slots' list.
 // move_kernel: the kept rows of keys, values and scales to the front. A CTA
 // looks up the places of its rows once and moves them for several heads, the
 // next head's rows on their way while one's are written. Row i comes from slot
@@ -23,12 +24,12 @@ namespace {
 using namespace w4kv;
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;
 constexpr int kMoveCtas = 4;        // CTAs an SM that the heads are shared out for
-constexpr int kHeldKeys = 16384;    // keys that a selecting CTA keeps in shared memory
+constexpr int kHeld = 16384;        // weights that a selecting CTA keeps in shared memory
 
 struct EvictParams {
   View c, d;
@@ -38,7 +39,7 @@ struct EvictParams {
   int32_t* list;  // the kept slots, rows of `ldlist`
   int64_t ldlist;
   int32_t pad;    // entries of a list row that are -1 behind the last (0: the caller wants no list)
-  float* kept_acc;  // their weights, rows of `ldkept_acc`
+  float* kept_acc;  // their weights, rows of `ldkept_acc` (where a CTA does not hold them)
   int64_t ldkept_acc;
   int32_t keep, recent;
   ErrorWord* err;
@@ -51,13 +52,12 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p, int32_t held_keys) {
-  extern __shared__ uint32_t keys[];  // of this CTA's slots, where there is room for them
-  __shared__ uint32_t hist[2][256];   // this CTA's counts: one pass fills one while others read the other
-  __shared__ uint32_t total[256];
-  __shared__ uint32_t picked[4];      // the digit, how many of it are wanted; this CTA's slots above and at it
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p, int32_t room) {
+  extern __shared__ float weights[];  // of this CTA's slots, where there is room for them
+  __shared__ __align__(16) uint32_t hist[4][256];  // this CTA's counts, a pass each
+  __shared__ uint32_t total[256];     // the cluster's
   __shared__ uint32_t counts[2];      // slots of this CTA that stay for sure, and at the threshold
-  __shared__ uint32_t warp_counts[kSelWarps];
+  __shared__ uint32_t warp_counts[2][32];
   pdl_launch_dependents();
   pdl_wait();
   cg::cluster_group cluster = cg::this_cluster();
@@ -94,77 +94,85 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     const bool none = want == 0;
     const int32_t chunk = ((n + ranks - 1) / ranks + 3) / 4 * 4;
     const int32_t c0 = min(n, rank * chunk), c1 = min(n, c0 + chunk), m1 = min(c1, m);
-    const bool held = chunk <= held_keys;
-    const auto key_of = [&](int32_t i) { return held ? keys[i - c0] : weight_key(acc[i]); };
-    if (tid < 256) hist[0][tid] = 0;
+    const bool held = chunk <= room;
+    const auto weight = [&](int32_t i) { return held ? weights[i - c0] : acc[i]; };
+    for (int i = tid; i < 4 * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
     __syncthreads();
+#pragma unroll 4
+    for (int32_t i = c0 + tid; i < c1; i += kSelThreads) {
+      const float w = acc[i];
+      if (held) weights[i - c0] = w;
+      if (i < m) atomicAdd(&hist[0][weight_key(w) >> 24], 1u);
+    }
+    sync_all();
     uint32_t prefix = 0, sure = 0, at_it = 0;  // the last two: this CTA's, of the slots that compete
     for (int pass = 0; pass < 4 && !none; ++pass) {
       const int shift = 24 - 8 * pass;
-      uint32_t* mine = hist[pass & 1];
-      if (pass == 0) {
+      const uint32_t* mine = hist[pass];
+      if (pass > 0) {
 #pragma unroll 4
         for (int32_t i = c0 + tid; i < m1; i += kSelThreads) {
-          const uint32_t k = weight_key(acc[i]);
-          if (held) keys[i - c0] = k;
-          atomicAdd(&mine[k >> 24], 1u);
+          const uint32_t k = weight_key(weight(i));
+          if ((k >> (shift + 8)) == prefix) atomicAdd(&hist[pass][(k >> shift) & 255u], 1u);
         }
-      } else {
-#pragma unroll 4
-        for (int32_t i = c0 + tid; i < m1; i += kSelThreads) {
-          const uint32_t k = key_of(i);
-          if ((k >> (shift + 8)) == prefix) atomicAdd(&mine[(k >> shift) & 255u], 1u);
+        sync_all();
+      }
+      // Each warp finds the digit: lane l sums digits 8 l .. 8 l + 7, the largest digits first.
+      uint32_t t[8], c[8], own = 0, own_c = 0;
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(mine + 8 * lane + j);
+        c[j] = x.x;
+        c[j + 1] = x.y;
+        c[j + 2] = x.z;
+        c[j + 3] = x.w;
+      }
+      if (ranks > 1) {
+        if (tid < 256) {
+          uint32_t sum = 0;
+          for (int r = 0; r < ranks; ++r) sum += cluster.map_shared_rank(hist[pass], r)[tid];
+          total[tid] = sum;
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = ranks > 1 ? total[8 * lane + j] : c[j];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        own += t[j];
+        own_c += c[j];
+      }
+      uint32_t above = own, above_c = own_c;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const uint32_t v = __shfl_down_sync(0xffffffffu, above, o), w = __shfl_down_sync(0xffffffffu, above_c, o);
+        if (lane + o < 32) {
+          above += v;
+          above_c += w;
         }
       }
-      sync_all();
-      if (tid < 256) {
-        uint32_t sum = mine[tid];
-        if (ranks > 1) {
-          sum = 0;
-          for (int r = 0; r < ranks; ++r) sum += cluster.map_shared_rank(mine, r)[tid];
-        }
-        total[tid] = sum;
-        hist[(pass + 1) & 1][tid] = 0;  // its readers are behind the barrier above
-      }
-      __syncthreads();
-      if (warp == 0) {
-        // lane l takes digits 8 l .. 8 l + 7, the largest digits first
-        uint32_t t[8], c[8], own = 0, own_c = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          t[j] = total[8 * lane + j];
-          c[j] = mine[8 * lane + j];
-          own += t[j];
-          own_c += c[j];
-        }
-        uint32_t above = own, above_c = own_c;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-          const uint32_t v = __shfl_down_sync(0xffffffffu, above, o), w = __shfl_down_sync(0xffffffffu, above_c, o);
-          if (lane + o < 32) {
-            above += v;
-            above_c += w;
-          }
-        }
-        above -= own;  // in the digits of the lanes above
-        above_c -= own_c;
+      above -= own;  // in the digits of the lanes above
+      above_c -= own_c;
+      const bool here = above < want && want <= above + own;
+      const int at = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+      uint32_t digit = 0, left = 0, higher = 0, same = 0;
+      if (here) {
 #pragma unroll
         for (int j = 7; j >= 0; --j) {
           if (above < want && want <= above + t[j]) {
-            picked[0] = 8 * lane + j;
-            picked[1] = want - above;
-            picked[2] = above_c;
-            picked[3] = c[j];
+            digit = 8 * lane + j;
+            left = want - above;
+            higher = above_c;
+            same = c[j];
           }
           above += t[j];
           above_c += c[j];
         }
       }
-      __syncthreads();
-      prefix = (prefix << 8) | picked[0];
-      want = picked[1];
-      sure += picked[2];
-      at_it = picked[3];
+      prefix = (prefix << 8) | __shfl_sync(0xffffffffu, digit, at);
+      want = __shfl_sync(0xffffffffu, left, at);
+      sure += __shfl_sync(0xffffffffu, higher, at);
+      at_it = __shfl_sync(0xffffffffu, same, at);
     }
     // `want` of the slots whose key is `prefix` stay, from the lowest on
     uint32_t sure_before = 0, at_before = 0;
@@ -180,14 +188,20 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
         at_before += other[1];
       }
     }
-    for (int32_t t0 = c0; t0 < c1; t0 += 4 * kSelThreads) {
+    // Where all CTAs hold their weights (each has as many slots as another or
+    // fewer) they have all been read, and may be written over.
+    float* out = held ? acc_out : kept_acc;
+    int turn = 0;
+    for (int32_t t0 = c0; t0 < c1; t0 += 4 * kSelThreads, turn ^= 1) {
       const int32_t i0 = t0 + 4 * tid;
       uint32_t is_sure = 0, is_at = 0;  // a bit for each of the four
+      float w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int32_t i = i0 + j;
+        w[j] = i < c1 ? weight(i) : 0.f;
+        const uint32_t k = weight_key(w[j]);
         if (i < m1) {
-          const uint32_t k = key_of(i);
           is_sure |= static_cast<uint32_t>(!none && k > prefix) << j;
           is_at |= static_cast<uint32_t>(!none && k == prefix) << j;
         } else if (i < c1) {
@@ -202,10 +216,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
         const uint32_t v = __shfl_up_sync(0xffffffffu, up, o);
         if (lane >= o) up += v;
       }
+      if (lane == 31) warp_counts[turn][warp] = up;
       __syncthreads();
-      if (lane == 31) warp_counts[warp] = up;
-      __syncthreads();
-      const uint32_t wc = warp_counts[lane];
+      const uint32_t wc = lane < kSelWarps ? warp_counts[turn][lane] : 0u;
       const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? wc : 0u) + up - own;
       const uint32_t all = __reduce_add_sync(0xffffffffu, wc);
       uint32_t g = sure_before + (before & 0xFFFFu), e = at_before + (before >> 16);
@@ -216,7 +229,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
           const int32_t at = static_cast<int32_t>(g + min(e, want));
           if (at < fresh) {
             list[at] = i0 + j;
-            kept_acc[at] = acc[i0 + j];
+            out[at] = w[j];
           }
         }
         g += a;
@@ -225,10 +238,11 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
       sure_before += all & 0xFFFFu;
       at_before += all >> 16;
     }
-    // every weight has been read: the kept ones may take their new places
-    __threadfence();
-    sync_all();
-    for (int32_t i = first; i < fresh; i += step) acc_out[i] = __ldcg(kept_acc + i);
+    if (!held) {  // every weight has been read once all are here: the kept ones may take their new places
+      __threadfence();
+      sync_all();
+      for (int32_t i = first; i < fresh; i += step) acc_out[i] = __ldcg(kept_acc + i);
+    }
   }
   for (int32_t i = fresh + first; i < n; i += step) acc_out[i] = 0.f;
   for (int32_t i = fresh + first; i < p.pad; i += step) list[i] = -1;
@@ -237,27 +251,30 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
   if (rank == 0 && tid == 0) p.d.lengths[b] = fresh;
 }
 
-// Where slot `slot`'s row of head 0 lies: elements into k and v, and its scale.
-__device__ __forceinline__ int64_t row_of(const View& c, int32_t b, int32_t slot, int64_t* scale, ErrorWord* err) {
+// Where slot `slot`'s row of head 0 lies: its number among the rows of k and v,
+// and among the scales.
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t row_of(const View& c, int32_t b, int32_t slot, uint32_t* scale, ErrorWord* err) {
   const int32_t index = c.page.quotient(slot);
   const int32_t page = page_of(c, b, index, err, w4dev::K_KV_EVICT);
-  if (page < 0) return -1;
-  const int32_t inner = slot - index * c.slots_per_page;
-  *scale = int64_t(page) * c.heads * c.slots_per_page + inner;
-  return int64_t(page) * c.page_stride + int64_t(inner) * c.dim;
+  if (page < 0) return kNoRow;
+  const uint32_t inner = slot - index * c.slots_per_page;
+  *scale = static_cast<uint32_t>(page) * (c.heads * c.slots_per_page) + inner;
+  return static_cast<uint32_t>(page) * c.page_rows + inner;
 }
 
 // A batch's rows of one head's keys or values.
+template <bool SCALES>
 struct Batch {
   uint4 x[kMoveUnroll];
-  float s[kMoveUnroll];
+  float s[SCALES ? kMoveUnroll : 1];
 };
 
 // vecs: 16-byte vectors of a row; per: those of this CTA's columns; in place
 // the grid's x is the column, elsewhere the batch (and per == vecs). y: a group
-// of `group` heads. rows_of: row and column of a thread.
-template <bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p, int vecs, int per, int elem, int group) {
+// of `group` heads.
+template <bool IN_PLACE, bool SCALES>
+__global__ void __launch_bounds__(kMoveThreads, 3) move_kernel(const EvictParams p, int vecs, int per, int group) {
   pdl_launch_dependents();
   pdl_wait();
   const int32_t b = blockIdx.z;
@@ -270,12 +287,11 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p,
   const int my_row = threadIdx.x / width, my_vec = column + threadIdx.x % width;
   const int rows = stride * kMoveUnroll;  // of a batch
   const bool live = my_row < stride;
-  const bool scales = p.c.ks != nullptr && my_vec == 0;
-  const int64_t head = int64_t(p.c.slots_per_page) * p.c.dim * elem;  // bytes from a head to the next
+  const bool scales = SCALES && my_vec == 0;
   int32_t r0 = IN_PLACE ? 0 : static_cast<int32_t>(min(int64_t(fresh), int64_t(blockIdx.x) * rows));
   const int32_t end = IN_PLACE ? fresh : min(fresh, r0 + rows);
   for (; r0 < end; r0 += rows) {
-    int64_t from[kMoveUnroll], to[kMoveUnroll], from_scale[kMoveUnroll], to_scale[kMoveUnroll];
+    uint32_t from[kMoveUnroll], to[kMoveUnroll], from_scale[kMoveUnroll], to_scale[kMoveUnroll];
     int32_t slot[kMoveUnroll];
 #pragma unroll
     for (int u = 0; u < kMoveUnroll; ++u) {
@@ -286,40 +302,40 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p,
     for (int u = 0; u < kMoveUnroll; ++u) {
       const int32_t r = r0 + u * stride + my_row;
       from_scale[u] = to_scale[u] = 0;
-      from[u] = to[u] = -1;
+      from[u] = to[u] = kNoRow;
       if (slot[u] >= 0 && !(IN_PLACE && slot[u] == r)) {
         from[u] = row_of(p.c, b, slot[u], &from_scale[u], p.err);
         to[u] = row_of(p.d, b, r, &to_scale[u], p.err);
-        if (from[u] < 0) to[u] = -1;
-        from[u] = from[u] * elem + 16 * my_vec;
-        if (to[u] >= 0) to[u] = to[u] * elem + 16 * my_vec;
+        if (from[u] == kNoRow) to[u] = kNoRow;
       }
     }
-    const auto load = [&](Batch& x, int i) {  // keys of heads h0 .. h1 - 1, then values
-      const int32_t h = i < h1 - h0 ? h0 + i : i - (h1 - h0) + h0;
-      const uint8_t* src = static_cast<const uint8_t*>(i < h1 - h0 ? p.c.k : p.c.v) + h * head;
-      const float* ss = (i < h1 - h0 ? p.c.ks : p.c.vs) + int64_t(h) * p.c.slots_per_page;
+    // step i: keys of heads h0 .. h1 - 1, then their values
+    const auto head = [&](int i) { return i < h1 - h0 ? h0 + i : i - (h1 - h0) + h0; };
+    const auto load = [&](Batch<SCALES>& x, int i) {
+      const uint32_t h = head(i) * p.c.slots_per_page;
+      const uint4* src = static_cast<const uint4*>(i < h1 - h0 ? p.c.k : p.c.v) + my_vec;
+      const float* ss = i < h1 - h0 ? p.c.ks : p.c.vs;
 #pragma unroll
       for (int u = 0; u < kMoveUnroll; ++u) {
-        if (to[u] >= 0) {
-          x.x[u] = *reinterpret_cast<const uint4*>(src + from[u]);
-          if (scales) x.s[u] = ss[from_scale[u]];
+        if (to[u] != kNoRow) {
+          x.x[u] = src[uint64_t(from[u] + h) * vecs];
+          if (scales) x.s[u] = ss[from_scale[u] + h];
         }
       }
     };
-    const auto store = [&](const Batch& x, int i) {
-      const int32_t h = i < h1 - h0 ? h0 + i : i - (h1 - h0) + h0;
-      uint8_t* dst = static_cast<uint8_t*>(i < h1 - h0 ? p.d.k : p.d.v) + h * head;
-      float* ds = (i < h1 - h0 ? p.d.ks : p.d.vs) + int64_t(h) * p.c.slots_per_page;
+    const auto store = [&](const Batch<SCALES>& x, int i) {
+      const uint32_t h = head(i) * p.c.slots_per_page;
+      uint4* dst = static_cast<uint4*>(i < h1 - h0 ? p.d.k : p.d.v) + my_vec;
+      float* ds = i < h1 - h0 ? p.d.ks : p.d.vs;
 #pragma unroll
       for (int u = 0; u < kMoveUnroll; ++u) {
-        if (to[u] >= 0) {
-          *reinterpret_cast<uint4*>(dst + to[u]) = x.x[u];
-          if (scales) ds[to_scale[u]] = x.s[u];
+        if (to[u] != kNoRow) {
+          dst[uint64_t(to[u] + h) * vecs] = x.x[u];
+          if (scales) ds[to_scale[u] + h] = x.s[u];
         }
       }
     };
-    Batch even, odd;
+    Batch<SCALES> even, odd;
     const int count = 2 * (h1 - h0);  // even
     load(even, 0);
     for (int i = 0; i < count; i += 2) {
@@ -415,17 +431,17 @@ extern "C" w4_status kv_evict(const kv_cache* src, const float* acc, int64_t lda
   unsigned ranks = 1;
   while (ranks < 8 && src->seqs * ranks * 2 <= di->sms && p.c.capacity / (ranks * 2) >= 2 * kSelThreads) ranks *= 2;
   const int64_t share = (p.c.capacity + ranks - 1) / ranks + 4;
-  const int32_t held_keys = share <= kHeldKeys ? static_cast<int32_t>(share) : kHeldKeys;
+  const int32_t room = share <= kHeld ? static_cast<int32_t>(share) : kHeld;
   static thread_local int ready = -1;
   if (ready != di->dev) {
-    const cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldKeys * 4);
+    const cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4);
     if (e != cudaSuccess) return cuda_fail(e, "kv_evict shared memory");
     ready = di->dev;
   }
   cudaError_t e = launch_pdl(select_kernel, dim3(static_cast<unsigned>(src->seqs) * ranks), kSelThreads,
-                             static_cast<size_t>(held_keys) * 4, st, ranks, false, p, held_keys);
+                             static_cast<size_t>(room) * 4, st, ranks, false, p, room);
   if (e != cudaSuccess) return cuda_fail(e, "launch kv_evict (select)");
-  const int elem = elem_bytes(src->type), vecs = src->head_dim * elem / 16;
+  const int vecs = src->head_dim * elem_bytes(src->type) / 16;
   const int64_t most = width < p.d.capacity ? width : p.d.capacity;
   if (most == 0) return W4_OK;
   // heads of a CTA: as many as leave every SM a few CTAs
@@ -436,10 +452,9 @@ extern "C" w4_status kv_evict(const kv_cache* src, const float* acc, int64_t lda
   while (group > 1 && pieces * src->seqs * ((src->kv_heads + group - 1) / group) < int64_t(kMoveCtas) * di->sms)
     group = (group + 1) / 2;
   const dim3 grid(static_cast<unsigned>(pieces), (src->kv_heads + group - 1) / group, static_cast<unsigned>(src->seqs));
-  if (in_place) {
-    e = launch_pdl(move_kernel<true>, grid, kMoveThreads, 0, st, 1, false, p, vecs, per, elem, group);
-  } else {
-    e = launch_pdl(move_kernel<false>, grid, kMoveThreads, 0, st, 1, false, p, vecs, per, elem, group);
-  }
+  void (*const move)(const EvictParams, int, int, int) =
+      src->type == W4_KV_I8 ? (in_place ? move_kernel<true, true> : move_kernel<false, true>)
+                            : (in_place ? move_kernel<true, false> : move_kernel<false, false>);
+  e = launch_pdl(move, grid, kMoveThreads, 0, st, 1, false, p, vecs, per, group);
   return e == cudaSuccess ? W4_OK : cuda_fail(e, "launch kv_evict (move)");
 }

@@ -13,8 +13,9 @@
 // rescaled and whether any of them can be an alternative. Each warp keeps its
 // best 32 keys sorted, one a lane, and drops what lies below the last wanted
 // one of any warp of the CTA (of n unordered logits about top * ln(n / top)
-// pass); to begin with, the top-th largest of the 32 lanes' first maxima is
-// such a bound. Bound by reading the logits, by latency where there are few.
+// pass); to begin with, the top-th largest of the threads' first maxima is such
+// a bound. Lists and sums are joined pairwise by as many warps. Bound by
+// reading the logits, by latency where there are few.
 #include <cooperative_groups.h>
 
 #include "kv_cache.cuh"
@@ -120,17 +121,46 @@ __device__ __forceinline__ Key merge(Key a, Key b, int lane) {
   return x;
 }
 
-// The lanes' keys sorted, the largest in lane 0.
-__device__ __forceinline__ Key sort(Key x, int lane) {
+// The lanes' values sorted, the largest in lane 0.
+__device__ __forceinline__ float sort(float x, int lane) {
 #pragma unroll
   for (int k = 2; k <= 32; k *= 2)
 #pragma unroll
     for (int o = k / 2; o > 0; o /= 2) {
-      const Key y = __shfl_xor_sync(0xffffffffu, x, o);
-      const bool larger = ((lane & o) == 0) == ((lane & k) == 0 || k == 32);
-      x = larger ? (x > y ? x : y) : (x < y ? x : y);
+      const float y = __shfl_xor_sync(0xffffffffu, x, o);
+      x = ((lane & o) == 0) == ((lane & k) == 0 || k == 32) ? fmaxf(x, y) : fminf(x, y);
     }
   return x;
+}
+
+// The largest 32 of two sorted lists of values, sorted.
+__device__ __forceinline__ float merge(float a, float b, int lane) {
+  float x = fmaxf(a, __shfl_sync(0xffffffffu, b, 31 - lane));
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) {
+    const float y = __shfl_xor_sync(0xffffffffu, x, o);
+    x = (lane & o) == 0 ? fmaxf(x, y) : fminf(x, y);
+  }
+  return x;
+}
+
+// The sums and lists of warps 0 .. count - 1 joined into warp 0's, in a fixed
+// order; every thread of the CTA calls it.
+template <bool TOP>
+__device__ __forceinline__ void join_all(Sums& s, Key& list, int count, Sums (&sums)[kWarpsLp],
+                                         Key (&keys)[TOP ? kWarpsLp : 1][32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int o = 1; o < count; o *= 2) {
+    if (warp < count && (warp & (2 * o - 1)) == o) {
+      if (lane == 0) sums[warp] = s;
+      if (TOP) keys[TOP ? warp : 0][lane] = list;
+    }
+    __syncthreads();
+    if ((warp & (2 * o - 1)) == 0 && warp + o < count) {
+      join(s, sums[warp + o]);
+      if (TOP) list = merge(list, keys[TOP ? warp + o : 0][lane], lane);
+    }
+  }
 }
 
 template <bool TOP>
@@ -140,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
   __shared__ Sums cta_sums;
   __shared__ Key cta_keys[32];
   __shared__ Key cta_bar;
+  __shared__ float sm_top[TOP ? kWarpsLp : 1][32];
   pdl_launch_dependents();
   pdl_wait();
   cg::cluster_group cluster = cg::this_cluster();
@@ -159,7 +190,6 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
   Key list = 0;
   Key bar = 0;  // a bound that the wanted keys of the CTA's part do not lie below, and its logit
   float bar_x = -INFINITY;
-  if (TOP && tid == 0) cta_bar = 0;
   const auto raise = [&](Key k) {
     if (k > bar) {
       bar = k;
@@ -185,7 +215,24 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
     }
   };
   if (q < q1) load(q);
-  if (TOP) __syncthreads();  // cta_bar is 0
+  if (TOP) {
+    // `top` logits lie at or above the top-th largest of the threads' first maxima
+    float top = -INFINITY;
+    if (q < q1) {
+#pragma unroll
+      for (int u = 0; u < kQuads; ++u) top = fmaxf(top, fmaxf(fmaxf(v[u].x, v[u].y), fmaxf(v[u].z, v[u].w)));
+    }
+    top = sort(top, lane);
+#pragma unroll
+    for (int o = 1; o < kWarpsLp; o *= 2) {
+      if ((warp & (2 * o - 1)) == o) sm_top[TOP ? warp : 0][lane] = top;
+      __syncthreads();
+      if ((warp & (2 * o - 1)) == 0) top = merge(top, sm_top[TOP ? warp + o : 0][lane], lane);
+    }
+    if (warp == 0 && lane == p.top - 1) cta_bar = top > -INFINITY ? logit_key(top, 0xFFFFFFFFu) : 0;
+    __syncthreads();
+    raise(cta_bar);
+  }
   if (warp == kWarpsLp - 1) {
     const int32_t tail = lead + 4 * quads;
     if (rank == 0 && lead > 0) {
@@ -201,7 +248,6 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
       if (TOP) offer(w[0], tail + lane, there);
     }
   }
-  bool begun = false;
   for (; q < q1; q += kQuads * kThreads) {
     float w[4 * kQuads];
 #pragma unroll
@@ -218,13 +264,6 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
     for (int i = 1; i < 4 * kQuads; ++i) top = fmaxf(top, w[i]);
     add(s, w, top);
     if (TOP) {
-      if (!begun) {
-        // a lane's maximum is a logit of its own (unless it is -Inf or NaN): `top` of them lie at or above the top-th
-        begun = true;
-        const Key k = top > -INFINITY ? logit_key(top, 0xFFFFFFFFu) : 0;
-        raise(shfl_key(sort(k, lane), p.top - 1));
-        if (lane == 0 && bar != 0) atomicMax(&cta_bar, bar);
-      }
       // NaN is never the maximum, and only matters where fewer than `top` others are there
       if (__any_sync(0xffffffffu, !(top < bar_x))) {
         raise(*static_cast<volatile Key*>(&cta_bar));
@@ -250,23 +289,22 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
                     __shfl_xor_sync(0xffffffffu, s.t, o)};
     join(s, b);
   }
-  if (lane == 0) sm_sums[warp] = s;
-  if (TOP) sm_keys[warp][lane] = list;
-  __syncthreads();
-  if (warp == 0) {
-    for (int w = 1; w < kWarpsLp; ++w) join(s, sm_sums[w]);
-    if (TOP) {
-      for (int w = 1; w < kWarpsLp; ++w) list = merge(list, sm_keys[w][lane], lane);
-      cta_keys[lane] = list;
+  join_all<TOP>(s, list, kWarpsLp, sm_sums, sm_keys);
+  if (ranks > 1) {
+    if (warp == 0) {
+      if (lane == 0) cta_sums = s;
+      if (TOP) cta_keys[lane] = list;
     }
-    if (lane == 0) cta_sums = s;
+    cluster.sync();
+    if (rank == 0) {
+      if (warp > 0 && warp < ranks) {
+        s = *cluster.map_shared_rank(&cta_sums, warp);
+        if (TOP) list = cluster.map_shared_rank(cta_keys, warp)[lane];
+      }
+      join_all<TOP>(s, list, ranks, sm_sums, sm_keys);
+    }
   }
-  cluster.sync();
   if (rank == 0 && warp == 0) {
-    for (int r = 1; r < ranks; ++r) {
-      join(s, *cluster.map_shared_rank(&cta_sums, r));
-      if (TOP) list = merge(list, cluster.map_shared_rank(cta_keys, r)[lane], lane);
-    }
     // l is 0 without a logit above -Inf, NaN with a NaN or +Inf: no distribution
     const float bad = __int_as_float(0x7fc00000);
     const bool none = !(s.l > 0.f);
@@ -291,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
         p.top_ids[row * p.top + lane] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(list));
     }
   }
-  cluster.sync();  // no CTA leaves while its shared memory is read
+  if (ranks > 1) cluster.sync();  // no CTA leaves while its shared memory is read
 }
 
 }  // namespace

@@ -26,6 +26,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kMaxRanks = 8;        // CTAs of a selecting cluster
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;
 constexpr int kMoveCtas = 4;        // CTAs an SM that the heads are shared out for
@@ -106,6 +107,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     }
     sync_all();
     uint32_t prefix = 0, sure = 0, at_it = 0;  // the last two: this CTA's, of the slots that compete
+    int low = 32;                              // `prefix` holds a key's bits from here on
     for (int pass = 0; pass < 4 && !none; ++pass) {
       const int shift = 24 - 8 * pass;
       const uint32_t* mine = hist[pass];
@@ -130,7 +132,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
       if (ranks > 1) {
         if (tid < 256) {
           uint32_t sum = 0;
-          for (int r = 0; r < ranks; ++r) sum += cluster.map_shared_rank(hist[pass], r)[tid];
+#pragma unroll
+          for (int r = 0; r < kMaxRanks; ++r)  // all on their way at once
+            if (r < ranks) sum += cluster.map_shared_rank(hist[pass], r)[tid];
           total[tid] = sum;
         }
         __syncthreads();
@@ -155,7 +159,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
       above_c -= own_c;
       const bool here = above < want && want <= above + own;
       const int at = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-      uint32_t digit = 0, left = 0, higher = 0, same = 0;
+      uint32_t digit = 0, left = 0, higher = 0, same = 0, all = 0;
       if (here) {
 #pragma unroll
         for (int j = 7; j >= 0; --j) {
@@ -164,6 +168,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
             left = want - above;
             higher = above_c;
             same = c[j];
+            all = t[j];
           }
           above += t[j];
           above_c += c[j];
@@ -173,8 +178,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
       want = __shfl_sync(0xffffffffu, left, at);
       sure += __shfl_sync(0xffffffffu, higher, at);
       at_it = __shfl_sync(0xffffffffu, same, at);
+      low = shift;
+      if (__shfl_sync(0xffffffffu, all, at) == want) break;  // all of this digit stay: the rest decides nothing
     }
-    // `want` of the slots whose key is `prefix` stay, from the lowest on
+    // `want` of the slots whose key begins with `prefix` stay, from the lowest on
     uint32_t sure_before = 0, at_before = 0;
     if (ranks > 1) {
       if (tid == 0) {
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
       for (int j = 0; j < 4; ++j) {
         const int32_t i = i0 + j;
         w[j] = i < c1 ? weight(i) : 0.f;
-        const uint32_t k = weight_key(w[j]);
+        const uint32_t k = none ? 0u : weight_key(w[j]) >> low;
         if (i < m1) {
           is_sure |= static_cast<uint32_t>(!none && k > prefix) << j;
           is_at |= static_cast<uint32_t>(!none && k == prefix) << j;
@@ -429,7 +436,7 @@ extern "C" w4_status kv_evict(const kv_cache* src, const float* acc, int64_t lda
   // one cluster per sequence: up to 8 CTAs while the sequences alone do not fill
   // the SMs and a CTA's share is a few thousand slots or more
   unsigned ranks = 1;
-  while (ranks < 8 && src->seqs * ranks * 2 <= di->sms && p.c.capacity / (ranks * 2) >= 2 * kSelThreads) ranks *= 2;
+  while (ranks < kMaxRanks && src->seqs * ranks * 2 <= di->sms && p.c.capacity / (ranks * 2) >= 2 * kSelThreads) ranks *= 2;
   const int64_t share = (p.c.capacity + ranks - 1) / ranks + 4;
   const int32_t room = share <= kHeld ? static_cast<int32_t>(share) : kHeld;
   static thread_local int ready = -1;

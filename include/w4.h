@@ -641,9 +641,10 @@ W4_API w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, int64
  *   length.
  * - kept: NULL, or int32 rows of `keep` entries ldkept apart: the kept slots'
  *   old places, -1 behind the last.
- * - workspace: kv_evict_workspace_size() bytes, 16-byte aligned, no zeroing,
- *   not shared by calls that may run at the same time. */
-W4_API size_t kv_evict_workspace_size(const kv_cache* src, int64_t keep);
+ * - workspace: kv_evict_workspace_size() bytes (with_kept: kept is given),
+ *   16-byte aligned, no zeroing, not shared by calls that may run at the same
+ *   time; may be NULL where that is 0. */
+W4_API size_t kv_evict_workspace_size(const kv_cache* src, int64_t keep, int32_t with_kept);
 W4_API w4_status kv_evict(const kv_cache* src, const float* acc, int64_t ldacc, int64_t keep, int64_t recent,
                           const kv_cache* dst, float* acc_out, int64_t ldacc_out, int32_t* kept, int64_t ldkept,
                           void* workspace, size_t workspace_bytes, void* stream);

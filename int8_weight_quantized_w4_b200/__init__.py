@@ -609,29 +609,31 @@ class KvCache:
 
 def _rows3(t, name: str, rows: int | None, heads: int | None, dim: int, device) -> int:
     """Row stride of an fp32 [rows, heads, dim] tensor whose rows are contiguous."""
-    if t.dim() != 3 or t.dtype is not _torch().float32 or t.device != device:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or t.dtype is not _torch().float32 or t.device != device:
         raise ValueError(f"{name} must be an fp32 [rows, heads, head_dim] tensor on {device}")
-    n, h, d = t.shape
+    n, h, d = shape
     if (rows is not None and n != rows) or (heads is not None and h != heads) or d != dim:
-        raise ValueError(f"{name} is {tuple(t.shape)}, expected [{rows}, {heads}, {dim}]")
-    s = t.stride()
-    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+        raise ValueError(f"{name} is {tuple(shape)}, expected [{rows}, {heads}, {dim}]")
+    if (d > 1 and stride[2] != 1) or (h > 1 and stride[1] != d):
         raise ValueError(f"a row of {name} must be contiguous")
-    return s[0] if n > 1 else h * d
+    return stride[0] if n > 1 else h * d
 
 
 def _vector(t, name: str, dtype, n: int, device) -> int:
-    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or t.device != device:
+    shape = t.shape
+    if len(shape) != 1 or shape[0] != n or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} [{n}] tensor on {device}")
     return t.data_ptr()
 
 
 def _matrix(t, name: str, dtype, n: int, width: int, device) -> int:
     """Row stride of an [n, >= width] tensor with contiguous rows."""
-    if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != n or t.shape[1] < width or t.device != device or \
-            (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != n or shape[1] < width or t.dtype is not dtype or t.device != device or \
+            (shape[1] > 1 and stride[1] != 1):
         raise ValueError(f"{name} must be a {dtype} [{n}, {width}] tensor with contiguous rows on {device}")
-    return t.stride(0) if n > 1 else max(width, 1)
+    return stride[0] if n > 1 else max(width, 1)
 
 
 class _On:
@@ -742,9 +744,10 @@ def kv_evict(cache: KvCache, acc, keep: int, recent: int = 0, dst: KvCache | Non
     ld = _matrix(acc, "acc", torch.float32, B, cache.capacity, dev)
     ldo = _matrix(acc_out, "acc_out", torch.float32, B, cache.capacity, dev)
     ldk = 0 if kept is None else _matrix(kept, "kept", torch.int32, B, keep, dev)
-    need = cache._need.get(keep)
+    key = (keep, kept is None, "evict")
+    need = cache._need.get(key)
     if need is None:
-        need = cache._need[keep] = int(lib().kv_evict_workspace_size(cache._ref, keep))
+        need = cache._need[key] = int(lib().kv_evict_workspace_size(cache._ref, keep, int(kept is not None)))
     if ws is None and need:
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     st = lib().kv_evict(cache._ref, acc.data_ptr(), ld, keep, recent, dst._ref, acc_out.data_ptr(), ldo, _ptr(kept),
@@ -767,12 +770,13 @@ def token_logprobs(logits, tokens=None, top: int = 0, stream=None):
     if _elsewhere(dev, stream):
         with _On(dev, stream):
             return token_logprobs(logits, tokens, top)
-    if logits.dim() == 1:
+    shape, f32 = logits.shape, torch.float32
+    if len(shape) != 2:
+        if len(shape) != 1:
+            raise ValueError("logits must be [M, V]")
         logits = logits.view(1, -1)
-    if logits.dim() != 2:
-        raise ValueError("logits must be [M, V]")
-    M, V = logits.shape
-    f32 = torch.float32
+        shape = logits.shape
+    M, V = shape
     ld = _matrix(logits, "logits", f32, M, V, dev)
     t = lp = tl = ti = 0
     logp = top_logp = top_ids = None

@@ -157,7 +157,7 @@ SIGNATURES = {
     "kv_attend": (C.c_int, [C.POINTER(KvCacheDesc), C.c_void_p, C.c_int64, C.c_int64, C.c_float, C.c_int64,
                             C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_size_t,
                             C.c_void_p]),
-    "kv_evict_workspace_size": (C.c_size_t, [C.POINTER(KvCacheDesc), C.c_int64]),
+    "kv_evict_workspace_size": (C.c_size_t, [C.POINTER(KvCacheDesc), C.c_int64, C.c_int32]),
     "kv_evict": (C.c_int, [C.POINTER(KvCacheDesc), C.c_void_p, C.c_int64, C.c_int64, C.c_int64,
                            C.POINTER(KvCacheDesc), C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p,
                            C.c_size_t, C.c_void_p]),

@@ -22,7 +22,7 @@ using namespace w4kv;
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kMostUnits = 4;
+constexpr int kMostUnits = 16;
 constexpr int kMaxLaneVecs = 2;  // float4s of a lane: 32 x 4 x 2 = 256, the largest head_dim
 
 // The kernels behind the attention kernel do not let the next one begin early,

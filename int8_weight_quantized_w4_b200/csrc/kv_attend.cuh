@@ -353,16 +353,18 @@ __device__ __forceinline__ void attend_runs(const AttendParams& p, uint8_t* smem
   Walk w;
   if (!find_run(p, w, run, scratch)) return;
   __syncthreads();
+  Segment s = {}, prev = {};
+  Queries<ROWS, Body::kWidth> queries;
   typename Body::Feed feed;
   feed.ahead.w = w;
+  bool more = next_segment(p, run, w, s);
+  if (more) queries.fetch(p, s);
   feed.ahead.open(p, run);
   feed.begin(p, run, smem + (threadIdx.x >> 5) * Body::Feed::kRing);
-  Segment s = {}, prev = {};
   for (int k = 0;; ++k) {
-    const bool more = next_segment(p, run, w, s);
-    Queries<ROWS, Body::kWidth> queries;
-    if (more) queries.fetch(p, s);
     if (k > 0) {
+      more = next_segment(p, run, w, s);
+      if (more) queries.fetch(p, s);
       __syncthreads();  // every warp has left the segment before
       finish<ROWS>(p, prev, k == 1, triple);
     }

@@ -359,17 +359,33 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 int64_t list_width(const View& c, int64_t keep) { return keep < c.capacity ? keep : c.capacity; }
 
-// [kept weights][kept slots], rows of the most that a sequence can keep
-size_t evict_bytes(const View& c, int64_t keep) {
-  return 2 * round256(static_cast<size_t>(c.seqs) * static_cast<size_t>(list_width(c, keep)) * 4);
+// CTAs of a sequence's cluster: up to 8 while the sequences alone do not fill
+// the SMs and a CTA's share is a thousand slots or more.
+unsigned select_ranks(const View& c, int sms) {
+  unsigned ranks = 1;
+  while (ranks < kMaxRanks && int64_t(c.seqs) * ranks * 2 <= sms && c.capacity / (ranks * 2) >= 2 * kSelThreads) ranks *= 2;
+  return ranks;
+}
+
+// The most slots of a CTA.
+int64_t select_share(const View& c, unsigned ranks) { return (int64_t(c.capacity) + ranks - 1) / ranks + 4; }
+
+// [kept weights, unless the CTAs hold them][kept slots, unless the caller gives
+// the room], rows of the most that a sequence can keep
+size_t kept_bytes(const View& c, int64_t keep) {
+  return round256(static_cast<size_t>(c.seqs) * static_cast<size_t>(list_width(c, keep)) * 4);
+}
+size_t evict_bytes(const View& c, int64_t keep, bool with_kept, int sms) {
+  return (select_share(c, select_ranks(c, sms)) > kHeld ? kept_bytes(c, keep) : 0) + (with_kept ? 0 : kept_bytes(c, keep));
 }
 
 }  // namespace
 
-extern "C" size_t kv_evict_workspace_size(const kv_cache* src, int64_t keep) {
+extern "C" size_t kv_evict_workspace_size(const kv_cache* src, int64_t keep, int32_t with_kept) {
   View c;
-  if (w4host::check_cache(src, "src", &c) != W4_OK || keep < 0) return 0;
-  return evict_bytes(c, keep);
+  const w4host::DeviceInfo* di = nullptr;
+  if (w4host::check_cache(src, "src", &c) != W4_OK || keep < 0 || w4host::current_device(&di) != W4_OK) return 0;
+  return evict_bytes(c, keep, with_kept != 0, di->sms);
 }
 
 extern "C" w4_status kv_evict(const kv_cache* src, const float* acc, int64_t ldacc, int64_t keep, int64_t recent,
@@ -409,7 +425,7 @@ extern "C" w4_status kv_evict(const kv_cache* src, const float* acc, int64_t lda
   const DeviceInfo* di = nullptr;
   rc = current_device(&di);
   if (rc != W4_OK) return rc;
-  const size_t need = evict_bytes(p.c, keep);
+  const size_t need = evict_bytes(p.c, keep, kept != nullptr, di->sms);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need))
     return fail(W4_ERR_WORKSPACE, "kv_evict needs a workspace of %zu bytes, %zu given", need,
                 workspace == nullptr ? size_t(0) : workspace_bytes);
@@ -422,22 +438,19 @@ extern "C" w4_status kv_evict(const kv_cache* src, const float* acc, int64_t lda
   p.recent = static_cast<int32_t>(recent);
   p.err = di->err;
   const int64_t width = list_width(p.c, keep);
-  p.kept_acc = static_cast<float*>(workspace);
-  p.ldkept_acc = width;
+  const unsigned ranks = select_ranks(p.c, di->sms);
+  const int64_t share = select_share(p.c, ranks);
+  p.kept_acc = static_cast<float*>(workspace);  // not used where the CTAs hold the weights
+  p.ldkept_acc = share > kHeld ? width : 0;
   if (kept != nullptr) {
     p.list = kept;
     p.ldlist = ldkept;
     p.pad = p.keep;
   } else {
-    p.list = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + need / 2);
+    p.list = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + (need - kept_bytes(p.c, keep)));
     p.ldlist = width;
   }
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // one cluster per sequence: up to 8 CTAs while the sequences alone do not fill
-  // the SMs and a CTA's share is a few thousand slots or more
-  unsigned ranks = 1;
-  while (ranks < kMaxRanks && src->seqs * ranks * 2 <= di->sms && p.c.capacity / (ranks * 2) >= 2 * kSelThreads) ranks *= 2;
-  const int64_t share = (p.c.capacity + ranks - 1) / ranks + 4;
   const int32_t room = share <= kHeld ? static_cast<int32_t>(share) : kHeld;
   static thread_local int ready = -1;
   if (ready != di->dev) {

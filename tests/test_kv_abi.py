@@ -64,7 +64,7 @@ def test_broken_descriptors_are_refused_before_any_launch(kw, status):
         assert st == status
         assert lib.w4_last_error()
     assert lib.kv_attend_workspace_size(C.byref(d), 4, 0) == 0
-    assert lib.kv_evict_workspace_size(C.byref(d), 4) == 0
+    assert lib.kv_evict_workspace_size(C.byref(d), 4, 0) == 0
 
 
 @pytest.mark.parametrize("kw,status", [

@@ -349,7 +349,7 @@ __device__ __forceinline__ void attend_runs(const AttendParams& p, uint8_t* smem
   __shared__ Run run;
   __shared__ float* triple[kWarps];
   float* sq = reinterpret_cast<float*>(smem + kWarps * Body::Feed::kRing);
-  float* body = sq + ROWS * Body::kWidth;
+  float* body = sq + ROWS * (Body::kWidth + 2);
   Walk w;
   if (!find_run(p, w, run, scratch)) return;
   __syncthreads();
@@ -385,8 +385,8 @@ __device__ __forceinline__ void attend_item(const AttendParams& p, uint8_t* smem
   cg::cluster_group cluster = cg::this_cluster();
   const int32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
   float* sq = reinterpret_cast<float*>(smem + kWarps * Body::Feed::kRing);
-  float* body = sq + ROWS * Body::kWidth;
-  float* mine = body + Body::kBodyFloats;  // this CTA's triple
+  float* body = sq + ROWS * (Body::kWidth + 2);
+  float* mine = sq;  // this CTA's triple, once no warp reads the queries
   const int32_t item = blockIdx.x / ranks, items = p.c.heads * p.chunks;
   const int D = p.c.dim;
   int32_t lo, n;
@@ -460,7 +460,7 @@ struct Ring {
   static constexpr int kStage = ((kNeed > TRIPLE * 4 ? kNeed : TRIPLE * 4) + 127) / 128 * 128;
   static constexpr int kRing = STAGES * kStage;
   static constexpr int kRows = 32 / CL;          // rows of a copy instruction
-  static constexpr uint32_t kAll = (1u << TS) - 1;  // every slot of a tile
+  static constexpr uint32_t kAll = 0xFFFFFFFFu >> (32 - TS);  // every slot of a tile
 
   Ahead<TS> ahead;
   Entry entry;              // of the tile to be copied next
@@ -531,12 +531,12 @@ struct Ring {
           }
         }
       }
-      if constexpr (I8) {  // a lane's key scale, or from lane TS on its value scale
-        const float* scales = lane < TS ? p.c.ks : p.c.vs;
-        if (there) scales += int64_t(entry.page) * (p.c.heads * p.c.slots_per_page) + entry.inner;
-        if (lane < 2 * TS)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + kScales + 4 * lane), "l"(scales),
-                       "r"(there ? 4 : 0)
+      if constexpr (I8) {  // keys' scales, then values': half the lanes each, or all of them twice
+        const int64_t scale = there ? int64_t(entry.page) * (p.c.heads * p.c.slots_per_page) + entry.inner : 0;
+#pragma unroll
+        for (int i = lane; i < 2 * TS; i += 32)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + kScales + 4 * i),
+                       "l"((i < TS ? p.c.ks : p.c.vs) + scale), "r"(there ? 4 : 0)
                        : "memory");
       }
     }
@@ -773,7 +773,7 @@ struct AttendKernel {
 template <class Body, int ROWS>
 AttendKernel attend_kernel_of() {
   return {attend_kernel<Body, ROWS>, attend_item_kernel<Body, ROWS>, ROWS, kWarps * Body::TS,
-          size_t(kWarps) * Body::Feed::kRing + (size_t(ROWS) * (2 * Body::kWidth + 2) + Body::kBodyFloats) * 4};
+          size_t(kWarps) * Body::Feed::kRing + (size_t(ROWS) * (Body::kWidth + 2) + Body::kBodyFloats) * 4};
 }
 
 // The kernel for a call of this element type (one translation unit a type).

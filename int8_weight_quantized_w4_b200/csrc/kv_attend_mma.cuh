@@ -97,7 +97,7 @@ struct MatrixLanes {
   static constexpr int VB = I8 && MAXD <= 64 ? 8 : 16;  // bytes of a value load
   static constexpr int VE = VB / E::kBytes;             // its elements
   static constexpr int NC = (MAXD / VE + 7) / 8;        // value vectors of a lane
-  static constexpr int NT = 1;                          // tiles of 16 slots at once
+  static constexpr int NT = I8 ? 2 : 1;                 // 16 slots each, at once: int8's stages have room for two
   static constexpr int TS = 16 * NT;
   static constexpr int kLift = 14;  // fp16 pieces: the exponent of the largest query, and of the largest weight
   static constexpr float kBelow = BF ? 0.f : kLift - kSlack;  // a new reference lies this far below the maximum

@@ -1,6 +1,8 @@
-// kv_attend's host side, and the small kernels behind the attention kernels:
-// join_kernel (partials of items that several CTAs shared) and gather_kernel
-// (attention weights summed over the query heads).
+// kv_attend's host side, and the small kernel behind the attention kernels: the
+// partials of items that several CTAs shared joined, and attention weights
+// summed over the query heads.
+#include <algorithm>
+
 #include "kv_attend.cuh"
 
 namespace w4kv {
@@ -23,19 +25,26 @@ using namespace w4kv;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kMostUnits = 16;
+constexpr int kGatherCtas = 16;  // CTAs an SM that the weights are shared out for
 constexpr int kMaxLaneVecs = 2;  // float4s of a lane: 32 x 4 x 2 = 256, the largest head_dim
 
-// The kernels behind the attention kernel do not let the next one begin early,
-// and ask for the attention's split of shared memory: a CTA of theirs that
-// lies between those of the next call's attention leaves room for one less on
-// its SM for as long as that runs (131072 slots of 8 x 128 bf16, call after
-// call: 117 us with either, 95 us without).
-//
-// One query head per `wpr` warps: wpr = 8 spreads the partials of a few long
-// rows, wpr = 1 passes over many rows that mostly have nothing to join.
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p, int wpr) {
+// The partials of an item: its first one, then the next CTAs' first ones.
+__device__ __forceinline__ const float* partial(const AttendParams& p, const int2& meta, int32_t i) {
+  const int64_t slot = i == 0 ? meta.x : 2 * int64_t(meta.x / 2 + i);
+  return p.part + slot * p.part_stride;
+}
+
+__device__ __forceinline__ int2 meta_of(const AttendParams& p, int32_t b, int32_t qh, int* row) {
+  const int32_t h = qh / p.group, in = qh - h * p.group, chunk = in / p.rows;
+  *row = in - chunk * p.rows;
+  return p.meta[(int64_t(b) * p.c.heads + h) * p.chunks + chunk];
+}
+
+// Query heads whose items several CTAs shared: `wpr` warps a head. wpr = 8
+// spreads the partials of a few long rows, wpr = 1 passes over many rows that
+// mostly have nothing to join.
+__device__ __forceinline__ void join_heads(const AttendParams& p, int wpr) {
   __shared__ Triple sm[kJoinWarps][32 * kMaxLaneVecs];
-  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int q_heads = p.c.heads * p.group;
   const int64_t row = int64_t(blockIdx.x) * (kJoinWarps / wpr) + warp / wpr;
@@ -50,15 +59,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
     b = static_cast<int32_t>(row / q_heads);
     qh = static_cast<int32_t>(row % q_heads);
     int32_t lo, n;
+    int g = 0;
     attended(p, b, lo, n);
-    int2 meta = make_int2(0, 0);
-    const int32_t h = qh / p.group, g = (qh % p.group) % p.rows;
-    if (n > lo) meta = p.meta[(int64_t(b) * p.c.heads + h) * p.chunks + (qh % p.group) / p.rows];
+    const int2 meta = n > lo ? meta_of(p, b, qh, &g) : make_int2(0, 0);
     work = meta.y != 1;
+#pragma unroll 2
     for (int32_t i = sub; i < (work ? meta.y : 0); i += wpr) {
-      // the first partial, then the next CTAs' first ones
-      const int64_t slot = i == 0 ? meta.x : 2 * int64_t(meta.x / 2 + i);
-      const float* part = p.part + slot * p.part_stride;
+      const float* part = partial(p, meta, i);
 #pragma unroll
       for (int j = 0; j < kMaxLaneVecs; ++j)
         if (lane + 32 * j < vecs) join(x[j], stored(part, p.rows, D, g, 4 * (lane + 32 * j)));
@@ -80,26 +87,51 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
     if (lane + 32 * j < vecs) write_out(p, b, qh, 4 * (lane + 32 * j), x[j]);
 }
 
+// A query head's log sum to base 2: as the attention kernel wrote it, or from
+// the partials, so that the weights need not wait for the join. -Inf: every
+// attended score is -Inf, and weighs nothing.
+__device__ __forceinline__ float lse2_of(const AttendParams& p, int32_t b, int32_t qh, bool runs) {
+  if (runs) {
+    int g;
+    const int2 meta = meta_of(p, b, qh, &g);
+    if (meta.y != 1) {
+      Triple x = no_slots();
+#pragma unroll 4
+      for (int32_t i = 0; i < meta.y; ++i) {
+        const float* part = partial(p, meta, i) + p.rows * p.c.dim;
+        join(x, {make_float4(0.f, 0.f, 0.f, 0.f), part[g], part[p.rows + g]});
+      }
+      return x.l == 0.f ? -INFINITY : x.m + log2f(x.l);
+    }
+  }
+  return p.lse2[int64_t(b) * p.c.heads * p.group + qh];
+}
+
 // acc[b, j] += sum over the query heads of 2^(x - lse2). A warp takes 32 slots
 // and every 8th head; the warps' sums are added in their order.
-__global__ void __launch_bounds__(kJoinThreads) gather_kernel(const AttendParams p, float* acc, int64_t ldacc) {
+__device__ __forceinline__ void gather_weights(const AttendParams& p, int block, int blocks, int32_t b, float* acc,
+                                               int64_t ldacc, bool runs) {
   __shared__ float sums[kJoinWarps][32];
-  pdl_wait();
+  __shared__ float z[kJoinThreads];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t b = blockIdx.y;
   const int q_heads = p.c.heads * p.group;
   int32_t lo, n;
   attended(p, b, lo, n);
-  const float* z = p.lse2 + int64_t(b) * q_heads;
-  for (int64_t j0 = lo + int64_t(blockIdx.x) * 32; j0 < n; j0 += int64_t(gridDim.x) * 32) {
+  for (int64_t j0 = lo + int64_t(block) * 32; j0 < n; j0 += int64_t(blocks) * 32) {
     const int64_t j = j0 + lane;
-    const float* x = p.scores + int64_t(b) * q_heads * p.c.capacity + j;
     float sum = 0.f;
-    if (j < n) {
+    for (int q0 = 0; q0 < q_heads; q0 += kJoinThreads) {
+      const int heads = min(kJoinThreads, q_heads - q0);
+      if (q_heads > kJoinThreads || j0 == lo + int64_t(block) * 32) {
+        __syncthreads();
+        if (threadIdx.x < heads) z[threadIdx.x] = lse2_of(p, b, q0 + threadIdx.x, runs);
+        __syncthreads();
+      }
+      const float* x = p.scores + (int64_t(b) * q_heads + q0) * p.c.capacity + j;
+      if (j < n) {
 #pragma unroll 4
-      for (int i = warp; i < q_heads; i += kJoinWarps) {
-        const float zi = z[i];  // -Inf: every attended score is -Inf, and weighs nothing
-        sum += zi == -INFINITY ? 0.f : ex2(x[int64_t(i) * p.c.capacity] - zi);
+        for (int i = warp; i < heads; i += kJoinWarps)
+          sum += z[i] == -INFINITY ? 0.f : ex2(x[int64_t(i) * p.c.capacity] - z[i]);
       }
     }
     sums[warp][lane] = sum;
@@ -110,6 +142,23 @@ __global__ void __launch_bounds__(kJoinThreads) gather_kernel(const AttendParams
       acc[int64_t(b) * ldacc + j] += sum;
     }
     __syncthreads();
+  }
+}
+
+// What is left behind the attention kernel: the first `joins` CTAs join, the
+// others gather weights, `per_seq` for each sequence. It does not let the next
+// kernel begin early, and asks for the attention's split of shared memory: a
+// CTA that lies between those of the next call's attention leaves room for one
+// less on its SM for as long as that runs (131072 slots of 8 x 128 bf16, call
+// after call: 117 us with either, 90 us without).
+__global__ void __launch_bounds__(kJoinThreads) behind_kernel(const AttendParams p, int joins, int wpr, int per_seq,
+                                                              float* acc, int64_t ldacc) {
+  pdl_wait();
+  if (blockIdx.x < joins) {
+    join_heads(p, wpr);
+  } else {
+    const int block = blockIdx.x - joins, b = block / per_seq;
+    gather_weights(p, block - b * per_seq, per_seq, b, acc, ldacc, joins > 0);
   }
 }
 
@@ -171,7 +220,7 @@ w4_status lay_out(const w4kv::View& c, int type, int64_t q_heads, bool with_acc,
   const w4_status rc = resident(L.kernel, &per_sm);
   if (rc != W4_OK) return rc;
   const int64_t items = int64_t(c.seqs) * c.heads * L.chunks;
-  const int64_t most = items * ((c.capacity + L.kernel.unit - 1) / L.kernel.unit + kOver);
+  const int64_t most = items * ((c.capacity + L.kernel.unit - 1) / L.kernel.unit + L.kernel.over);
   if (most > 0x7fffffff) return w4host::fail(W4_ERR_SHAPE, "seqs x heads x capacity are more slots than a call takes");
   const int64_t wave = int64_t(per_sm) * sms;
   // An item a cluster: the widest of up to 16 CTAs that one wave holds for all
@@ -265,29 +314,33 @@ extern "C" w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, i
   p.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.group = static_cast<int32_t>(q_heads / c->kv_heads);
   p.rows = L.kernel.rows;
+  p.over = L.kernel.over;
   while ((1 << p.unit_log) < L.kernel.unit) ++p.unit_log;
   p.q_vec = (bits(q) & 15) == 0 && (c->seqs <= 1 || ldq % 4 == 0);
   p.chunks = L.chunks;
   p.err = di->err;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (L.ranks != 0) {
-    e = launch_pdl(L.kernel.item_fn, dim3(L.ctas), kAttendThreads, L.kernel.smem, st, L.ranks, true, p);
-  } else {
-    e = launch_pdl(L.kernel.fn, dim3(L.ctas), kAttendThreads, L.kernel.smem, st, 1, true, p);
-    if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend");
-    const int64_t rows = c->seqs * q_heads;
-    const int wpr = rows <= int64_t(di->sms) * kJoinWarps ? kJoinWarps : 1;
-    const int64_t rows_per_cta = kJoinWarps / wpr;
-    e = launch_pdl(join_kernel, dim3(static_cast<unsigned>((rows + rows_per_cta - 1) / rows_per_cta)), kJoinThreads, 0,
-                   st, 1, true, p, wpr);
-  }
+  cudaError_t e = launch_pdl(L.ranks != 0 ? L.kernel.item_fn : L.kernel.fn, dim3(L.ctas), kAttendThreads, L.kernel.smem,
+                             st, L.ranks != 0 ? L.ranks : 1, true, p);
   if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend");
+  int64_t joins = 0, gathers = 0, per_seq = 1;
+  int wpr = 1;
+  if (L.ranks == 0) {
+    const int64_t rows = c->seqs * q_heads;
+    wpr = rows <= int64_t(di->sms) * kJoinWarps ? kJoinWarps : 1;
+    const int64_t rows_per_cta = kJoinWarps / wpr;
+    joins = (rows + rows_per_cta - 1) / rows_per_cta;
+  }
   if (acc != nullptr && p.c.capacity > 0) {
-    const int64_t per_row = (p.c.capacity + 31) / 32;
-    const dim3 grid(static_cast<unsigned>(per_row < 1024 ? per_row : 1024), static_cast<unsigned>(c->seqs));
-    e = launch_pdl(gather_kernel, grid, kJoinThreads, 0, st, 1, true, p, acc, ldacc);
-    if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend (weights)");
+    const int64_t tiles = (int64_t(p.c.capacity) + 31) / 32;
+    const int64_t fair = std::max<int64_t>(1, int64_t(kGatherCtas) * di->sms / c->seqs);
+    per_seq = std::min(tiles, fair);
+    gathers = per_seq * c->seqs;
+  }
+  if (joins + gathers > 0) {
+    e = launch_pdl(behind_kernel, dim3(static_cast<unsigned>(joins + gathers)), kJoinThreads, 0, st, 1, true, p,
+                   static_cast<int>(joins), wpr, static_cast<int>(per_seq), acc, ldacc);
+    if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend (join)");
   }
   return W4_OK;
 }

@@ -14,9 +14,9 @@
 // dealt to the CTAs in equal contiguous runs, by the lengths on the device: a
 // batch of unequal lengths, one long sequence and many short ones all load
 // every SM alike, and a CUDA graph stays valid while the lengths grow. An item
-// counts kOver units more than it has, what beginning and ending it costs. A
+// counts a unit or two more than it has, what beginning and ending it costs. A
 // CTA holds at most one item that began before its run and one that goes on
-// behind it; those leave (m, l, a) in the workspace and join_kernel joins them
+// behind it; those leave (m, l, a) in the workspace and behind_kernel joins them
 // in the order of the slots. So no result depends on timing, and nothing has
 // to be zero beforehand. Where one wave of clusters holds all items with a few
 // units for each CTA, an item is a cluster instead, and its CTAs join theirs
@@ -43,8 +43,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 7.f;  // see the bodies: how far, to base 2, a maximum may pass its reference
 
-constexpr int kOver = 1;  // an item's own cost, in units
-
 struct AttendParams {
   View c;
   const float* q;
@@ -59,6 +57,7 @@ struct AttendParams {
   float scale2;    // scale * log2 e
   int32_t group, rows, chunks;  // query heads of a key-value head, of an item, items of a key-value head
   int32_t unit_log;             // slots of a unit: a tile for each warp
+  int32_t over;                 // an item's own cost, in units
   int32_t q_vec;                // the rows of q are 16-byte aligned
   ErrorWord* err;
 };
@@ -77,7 +76,7 @@ __device__ __forceinline__ int32_t units_of(const AttendParams& p, int32_t slots
 __device__ __forceinline__ int32_t cost_of(const AttendParams& p, int32_t b) {
   int32_t lo, n;
   attended(p, b, lo, n);
-  return n > lo ? units_of(p, n - lo) + kOver : 0;
+  return n > lo ? units_of(p, n - lo) + p.over : 0;
 }
 
 // How the units are dealt (shared by the CTA): each CTA takes `share` of them,
@@ -93,7 +92,7 @@ struct Run {
   }
 };
 
-// What is left of this CTA's run, in units that count kOver more an item.
+// What is left of this CTA's run, in units that count `over` more an item.
 struct Walk {
   int32_t left;
   int32_t b, item, unit;  // sequence, item within it, unit within that
@@ -183,9 +182,9 @@ __device__ __forceinline__ bool next_segment(const AttendParams& p, const Run& r
       w.n = -1;
       continue;
     }
-    const int32_t units = units_of(p, w.n - w.lo), cost = units + kOver;
+    const int32_t units = units_of(p, w.n - w.lo), cost = units + p.over;
     const int32_t stop = min(cost - w.unit, w.left) + w.unit;
-    const int32_t from = max(0, w.unit - kOver), to = max(0, stop - kOver);
+    const int32_t from = max(0, w.unit - p.over), to = max(0, stop - p.over);
     const int32_t last = run.end - w.left + (cost - w.unit) - 1;  // the item's last unit
     s.b = w.b;
     s.item = w.item;
@@ -594,6 +593,7 @@ struct PlainLanes {
   static constexpr int TS = NP * RPW;
   static constexpr int kWidth = LPR * VPL * EPV;  // of a row of queries in shared memory
   static constexpr int kBodyFloats = 0;
+  static constexpr int kOver = 1;
   static constexpr int kMinCtas = GT * VPL * EPV <= 16 ? 5 : (GT * VPL * EPV <= 32 ? 4 : (GT * VPL * EPV <= 64 ? 3 : 2));
   using Feed = Ring<TYPE, TS, LPR, VPL, LPR * VPL, false, 2, GT * (kWidth + 2)>;
 
@@ -767,12 +767,13 @@ struct AttendKernel {
   void (*item_fn)(const AttendParams);  // an item a cluster
   int rows;         // query heads of an item
   int unit;         // slots of a unit
+  int over;         // an item's own cost, in units
   size_t smem;      // bytes of shared memory
 };
 
 template <class Body, int ROWS>
 AttendKernel attend_kernel_of() {
-  return {attend_kernel<Body, ROWS>, attend_item_kernel<Body, ROWS>, ROWS, kWarps * Body::TS,
+  return {attend_kernel<Body, ROWS>, attend_item_kernel<Body, ROWS>, ROWS, kWarps * Body::TS, Body::kOver,
           size_t(kWarps) * Body::Feed::kRing + (size_t(ROWS) * (Body::kWidth + 2) + Body::kBodyFloats) * 4};
 }
 

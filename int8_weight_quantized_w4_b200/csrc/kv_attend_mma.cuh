@@ -104,6 +104,7 @@ struct MatrixLanes {
   static constexpr int kFrag = SETS * STEPS * 32 * 4;   // words of the queries' operands
   static constexpr int kWidth = MAXD;  // of a row of queries in shared memory
   static constexpr int kBodyFloats = kFrag;
+  static constexpr int kOver = 2;  // 5 us of a segment's own against 2 to 3 us a unit
   static constexpr int kMinCtas = 3;
   static constexpr int CV = MAXD == 96 ? 3 : 1;         // copies: lanes of a row, vectors of a lane
   static constexpr int CL = MAXD / EPV / CV;

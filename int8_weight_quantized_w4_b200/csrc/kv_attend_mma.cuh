@@ -104,7 +104,7 @@ struct MatrixLanes {
   static constexpr int kFrag = SETS * STEPS * 32 * 4;   // words of the queries' operands
   static constexpr int kWidth = MAXD;  // of a row of queries in shared memory
   static constexpr int kBodyFloats = kFrag;
-  static constexpr int kOver = 2;  // 5 us of a segment's own against 2 to 3 us a unit
+  static constexpr int kOver = 3;  // beginning and ending a segment takes about 5 us, a unit 2 to 3 us
   static constexpr int kMinCtas = 3;
   static constexpr int CV = MAXD == 96 ? 3 : 1;         // copies: lanes of a row, vectors of a lane
   static constexpr int CL = MAXD / EPV / CV;
@@ -191,7 +191,7 @@ struct MatrixLanes {
       for (int n = 0; n < 2 * NT; ++n)
 #pragma unroll
         for (int i = 0; i < NI; ++i) kx[n][i] = *reinterpret_cast<const uint4*>(stage + Feed::place(8 * n + g, t + 4 * i));
-      float c[2 * NT][4] = {}, odd[2 * NT][4] = {};  // int8 has the registers for two chains of products
+      float c[2 * NT][4] = {};
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
         const int i = st / (EPV / 4), j = st % (EPV / 4);
@@ -210,14 +210,9 @@ struct MatrixLanes {
             b1 = word(kx[n][i], 2 * j + 1);
           }
 #pragma unroll
-          for (int s = 0; s < SETS; ++s) mma16816<TYPE>(I8 && (st & 1) ? odd[n] : c[n], a[s], b0, b1);
+          for (int s = 0; s < SETS; ++s) mma16816<TYPE>(c[n], a[s], b0, b1);
         }
       }
-#pragma unroll
-      for (int n = 0; n < 2 * NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if constexpr (I8) c[n][e] += odd[n][e];
       VVec vx[4 * NT][NC];
 #pragma unroll
       for (int n = 0; n < 4 * NT; ++n)

@@ -2,11 +2,12 @@
 // descriptor checks that the cache's entry points share.
 //
 // Bound by its bytes (fp32 rows in, stored rows out) for prompts and by
-// latency for a decode step. A token is one CTA, so that its place in the
-// cache (a search in cu_tokens, the length, the page: three dependent reads)
-// is found once, while the token's first 32 KB are already on their way. int8
-// rows go to half-warps, 16 lanes of 4 elements wide, which a row's maximum is
-// reduced over; the others are copied as they come, 4 elements a thread.
+// latency for a decode step. A token is one CTA, or a few warps of one where it
+// is short, so that its place in the cache (a search in cu_tokens, the length,
+// the page: three dependent reads) is found once, while the token's first
+// values are already on their way. int8 rows go to half-warps, 16 lanes of 4
+// elements wide, which a row's maximum is reduced over; the others are copied
+// as they come, 4 elements a thread.
 #include "kv_cache.cuh"
 
 namespace w4host {
@@ -76,7 +77,7 @@ using namespace w4kv;
 
 constexpr int kThreads = 256;
 constexpr int kRowLanes = 16;
-constexpr int kRowVecs = 4;  // of 4 elements: 16 lanes x 4 x 4 = 256, the largest head_dim
+constexpr float kSmallScale = 1e-30f;  // below it the inverse may overflow
 
 struct AppendParams {
   View c;
@@ -88,6 +89,7 @@ struct AppendParams {
   int32_t* lengths_out;  // NULL: written by advance_kernel
   int32_t vec;           // both inputs' rows are 16-byte aligned
   Divisor quads;         // float4s of a row of head_dim elements
+  int32_t group_log;     // threads of a token
   ErrorWord* err;
 };
 
@@ -150,21 +152,22 @@ struct Copied {
   static constexpr int kAhead = 8;
   float4 x[kAhead];
 
-  __device__ __forceinline__ void load(const AppendParams& p, int64_t t, int32_t from) {
+  __device__ __forceinline__ void load(const AppendParams& p, int64_t t, int32_t from, int32_t tid) {
     const int32_t half = p.c.heads * p.c.dim / 4;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int32_t i = from + threadIdx.x + j * kThreads;
+      const int32_t i = from + tid + (j << p.group_log);
       if (i < half) x[j] = load4(p, p.k + t * p.ldk + 4 * i);
       else if (i < 2 * half) x[j] = load4(p, p.v + t * p.ldv + 4 * (i - half));
     }
   }
   // page_at: elements to the page; inner: the slot in it
-  __device__ __forceinline__ void store(const AppendParams& p, int64_t page_at, int32_t inner, int32_t from) const {
+  __device__ __forceinline__ void store(const AppendParams& p, int64_t page_at, int32_t inner, int32_t from,
+                                        int32_t tid) const {
     const int32_t half = p.c.heads * p.c.dim / 4;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int32_t i = from + threadIdx.x + j * kThreads;
+      const int32_t i = from + tid + (j << p.group_log);
       if (i < 2 * half) {
         const int32_t r = i < half ? i : i - half, h = p.quads.quotient(r), d = r - h * (p.c.dim / 4);
         const int64_t at = page_at + (int64_t(h) * p.c.slots_per_page + inner) * p.c.dim + 4 * d;
@@ -174,32 +177,34 @@ struct Copied {
   }
 };
 
-// int8: a row of head_dim elements for each 16 lanes, keys' rows, then values'.
+// int8: a row of head_dim elements for each 16 lanes, VECS float4s a lane; keys'
+// rows, then values'.
+template <int VECS>
 struct Quantised {
-  float4 x[kRowVecs];
+  float4 x[VECS];
 
-  __device__ __forceinline__ void load(const AppendParams& p, int64_t t, int32_t from) {
+  __device__ __forceinline__ void load(const AppendParams& p, int64_t t, int32_t from, int32_t tid) {
     const int lane = threadIdx.x % kRowLanes;
-    const int32_t r = from + threadIdx.x / kRowLanes;
+    const int32_t r = from + tid / kRowLanes;
     const float* src = r < p.c.heads ? p.k + t * p.ldk + int64_t(r) * p.c.dim : p.v + t * p.ldv + int64_t(r - p.c.heads) * p.c.dim;
 #pragma unroll
-    for (int i = 0; i < kRowVecs; ++i) {
+    for (int i = 0; i < VECS; ++i) {
       const int at = lane + i * kRowLanes;
       x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < 2 * p.c.heads && at < p.c.dim / 4) x[i] = load4(p, src + 4 * at);
     }
   }
-  __device__ __forceinline__ void store(const AppendParams& p, int32_t page, int32_t inner, int32_t from) {
+  __device__ __forceinline__ void store(const AppendParams& p, int32_t page, int32_t inner, int32_t from, int32_t tid) {
     const View& c = p.c;
     const int lane = threadIdx.x % kRowLanes;
-    const int32_t r = from + threadIdx.x / kRowLanes;
+    const int32_t r = from + tid / kRowLanes;
     const bool live = r < 2 * c.heads, is_v = r >= c.heads;
     const int32_t h = is_v ? r - c.heads : r;
     float top = 0.f, poison = 0.f;  // NaN for an Inf or NaN in the row
 #pragma unroll
-    for (int i = 0; i < kRowVecs; ++i) {
+    for (int i = 0; i < VECS; ++i) {
       top = fmaxf(fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y))), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
-      poison += x[i].x * 0.f + x[i].y * 0.f + (x[i].z * 0.f + x[i].w * 0.f);
+      poison = fmaf(x[i].x, 0.f, fmaf(x[i].y, 0.f, fmaf(x[i].z, 0.f, fmaf(x[i].w, 0.f, poison))));
     }
 #pragma unroll
     for (int o = kRowLanes / 2; o > 0; o /= 2) {
@@ -209,59 +214,80 @@ struct Quantised {
     // the fp64 quotient rounded to fp32 is the correctly rounded fp32 one
     const bool bad = poison != 0.f;
     const float sc = bad ? __int_as_float(0x7fc00000) : (top > 0.f ? __fdiv_rn(top, 127.f) : 1.f);
-    // a scale that underflows to 0 stores zeros, which it also stands for
-    const double s = bad || sc == 0.f ? static_cast<double>(INFINITY) : static_cast<double>(sc);
     if (!live) return;
     const int64_t row = int64_t(h) * c.slots_per_page + inner;
     if (lane == 0) (is_v ? c.vs : c.ks)[int64_t(page) * c.heads * c.slots_per_page + row] = sc;
-    uint8_t* base = static_cast<uint8_t*>(is_v ? c.v : c.k) + int64_t(page) * c.page_stride + row * c.dim;
+    uint32_t* base = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(is_v ? c.v : c.k) + int64_t(page) * c.page_stride +
+                                                 row * c.dim);
+    // a scale that underflows to 0 stores zeros, which it also stands for
+    const bool zeros = bad || sc == 0.f;
+    const float inverse = sc >= kSmallScale ? 1.f / sc : __int_as_float(0x7fc00000);  // NaN: every code the long way
 #pragma unroll
-    for (int i = 0; i < kRowVecs; ++i) {
+    for (int i = 0; i < VECS; ++i) {
       const int at = lane + i * kRowLanes;
-      if (at < c.dim / 4)
-        reinterpret_cast<uint32_t*>(base)[at] =
-            bad ? 0u : code(x[i].x, s) | code(x[i].y, s) << 8 | code(x[i].z, s) << 16 | code(x[i].w, s) << 24;
+      if (at < c.dim / 4) base[at] = zeros ? 0u : codes(x[i], sc, inverse);
     }
   }
-  // The quotient in fp64, as the definition has it: an fp32 quotient rounds
-  // some values onto a half and then to another code.
-  __device__ static __forceinline__ uint32_t code(float f, double s) {
-    const double q = rint(static_cast<double>(f) / s);
-    return static_cast<uint32_t>(static_cast<int>(fmin(fmax(q, -127.0), 127.0))) & 0xFFu;
+  // rint(x / s) of the fp64 quotient, as the definition has it, of four x. x
+  // times the rounded inverse is off by at most 3 roundings, 127 x 3 x 2^-24 =
+  // 2.3e-5, so only a value within that of a half can round to another code and
+  // takes the quotient itself. 1.5 x 2^23 + x rounds x to an integer, whose low
+  // byte is the sum's. (7254 tokens of 32 x 96: all by quotients 139 us.)
+  __device__ static __forceinline__ uint32_t codes(float4 f, float s, float inverse) {
+    const float t[4] = {f.x * inverse, f.y * inverse, f.z * inverse, f.w * inverse};
+    uint32_t b[4];
+    bool sure = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float m = __fadd_rn(t[i], 12582912.f);
+      sure = sure && fabsf(t[i] - __fadd_rn(m, -12582912.f)) < 0.49995f;
+      b[i] = __float_as_uint(m);
+    }
+    if (!sure) {
+      const float g[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const double q = rint(static_cast<double>(g[i]) / static_cast<double>(s));
+        b[i] = static_cast<uint32_t>(static_cast<int>(fmin(fmax(q, -127.0), 127.0)));
+      }
+    }
+    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
   }
 };
 
-template <int TYPE>
+// VECS: int8 only, float4s of a lane (head_dim up to 64 VECS).
+template <int TYPE, int VECS>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
   constexpr bool I8 = TYPE == W4_KV_I8;
   pdl_launch_dependents();
   pdl_wait();
   const View& c = p.c;
-  typename std::conditional<I8, Quantised, Copied<TYPE>>::type data;
-  const int32_t step = I8 ? kThreads / kRowLanes : Copied<TYPE>::kAhead * kThreads;
+  using Data = typename std::conditional<I8, Quantised<VECS>, Copied<TYPE>>::type;
+  Data data;
+  const int32_t threads = 1 << p.group_log, tid = threadIdx.x & (threads - 1);
+  const int32_t step = I8 ? threads / kRowLanes : Copied<TYPE>::kAhead * threads;
   const int32_t count = I8 ? 2 * c.heads : 2 * c.heads * c.dim / 4;
-  const int64_t t = blockIdx.x;
-  if (t < p.tokens) data.load(p, t, 0);
+  const int64_t t = int64_t(blockIdx.x) * (kThreads >> p.group_log) + (threadIdx.x >> p.group_log);
+  if (t < p.tokens) data.load(p, t, 0, tid);
   // the new lengths, where they go to memory of their own
   const int64_t b_of_thread = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   if (p.lengths_out != nullptr && p.cu != nullptr && b_of_thread < c.seqs)
     p.lengths_out[b_of_thread] = advanced(p, static_cast<int32_t>(b_of_thread));
-  if (t >= p.tokens) return;
-  int32_t b = static_cast<int32_t>(t), slot;
+  int32_t b = static_cast<int32_t>(t), slot = 0;
   if (p.cu == nullptr) {
-    slot = held_length(c, b, p.err, w4dev::K_KV_APPEND);
-    if (p.lengths_out != nullptr) {  // this CTA alone reads lengths[b], so it may be advanced in place
-      __syncthreads();
-      if (threadIdx.x == 0) p.lengths_out[b] = min(slot + 1, c.capacity);
-    }
-  } else {
+    if (t < p.tokens) slot = held_length(c, b, p.err, w4dev::K_KV_APPEND);
+    __syncthreads();  // these threads alone read lengths[b], so it may be advanced in place
+    if (t < p.tokens && tid == 0) p.lengths_out[b] = min(slot + 1, c.capacity);
+  }
+  if (t >= p.tokens) return;
+  if (p.cu != nullptr) {
     b = sequence_of(p, t);
     if (b >= c.seqs || p.cu[b] > t || p.cu[b + 1] <= t) return;  // a row of no sequence
     const int64_t at = held_length(c, b, p.err, w4dev::K_KV_APPEND) + (t - p.cu[b]);
     slot = static_cast<int32_t>(at < c.capacity ? at : c.capacity);
   }
   if (slot >= c.capacity) {
-    if (threadIdx.x == 0) w4dev::record_error(p.err, W4_ERR_VALUE, w4dev::K_KV_APPEND, b);
+    if (tid == 0) w4dev::record_error(p.err, W4_ERR_VALUE, w4dev::K_KV_APPEND, b);
     return;
   }
   const int32_t index = c.page.quotient(slot);
@@ -269,11 +295,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
   if (page < 0) return;
   const int32_t inner = slot - index * c.slots_per_page;
   for (int32_t from = 0; from < count; from += step) {
-    if (from > 0) data.load(p, t, from);
     if constexpr (I8) {
-      data.store(p, page, inner, from);
+      Data next;  // a row's rounding takes as long as the next one's loads
+      if (from + step < count) next.load(p, t, from + step, tid);
+      data.store(p, page, inner, from, tid);
+      data = next;
     } else {
-      data.store(p, int64_t(page) * c.page_stride, inner, from);
+      if (from > 0) data.load(p, t, from, tid);
+      data.store(p, int64_t(page) * c.page_stride, inner, from, tid);
     }
   }
 }
@@ -326,16 +355,24 @@ extern "C" w4_status kv_append(const kv_cache* c, const float* k, int64_t ldk, c
   p.vec = ((bits(k) | bits(v)) & 15) == 0 && (tokens <= 1 || ((ldk | ldv) & 3) == 0);
   const bool in_place = cu_tokens != nullptr && lengths_out == c->lengths;
   p.lengths_out = in_place ? nullptr : lengths_out;
-  const int64_t by_seq = (c->seqs + kThreads - 1) / kThreads;
-  const dim3 grid(static_cast<unsigned>(tokens > by_seq ? tokens : by_seq));
+  // threads of a token: as many as its first loads keep busy (int8: a half-warp for each row)
+  const int64_t busy = c->type == W4_KV_I8 ? 2 * int64_t(c->kv_heads) * kRowLanes : 2 * wide / 4 / Copied<W4_KV_F32>::kAhead;
+  p.group_log = 5;
+  while ((1 << p.group_log) < busy && (1 << p.group_log) < kThreads) ++p.group_log;
+  const int64_t by_seq = (c->seqs + kThreads - 1) / kThreads, per_cta = kThreads >> p.group_log;
+  const int64_t by_token = (tokens + per_cta - 1) / per_cta;
+  const dim3 grid(static_cast<unsigned>(by_token > by_seq ? by_token : by_seq));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  switch (c->type) {
-    case W4_KV_F32: e = launch_pdl(append_kernel<W4_KV_F32>, grid, kThreads, 0, st, 1, false, p); break;
-    case W4_KV_F16: e = launch_pdl(append_kernel<W4_KV_F16>, grid, kThreads, 0, st, 1, false, p); break;
-    case W4_KV_BF16: e = launch_pdl(append_kernel<W4_KV_BF16>, grid, kThreads, 0, st, 1, false, p); break;
-    default: e = launch_pdl(append_kernel<W4_KV_I8>, grid, kThreads, 0, st, 1, false, p); break;
+  void (*kernel)(const AppendParams) = append_kernel<W4_KV_F32, 1>;
+  if (c->type == W4_KV_F16) kernel = append_kernel<W4_KV_F16, 1>;
+  if (c->type == W4_KV_BF16) kernel = append_kernel<W4_KV_BF16, 1>;
+  if (c->type == W4_KV_I8) {
+    kernel = c->head_dim <= 64    ? append_kernel<W4_KV_I8, 1>
+             : c->head_dim <= 128 ? append_kernel<W4_KV_I8, 2>
+             : c->head_dim <= 192 ? append_kernel<W4_KV_I8, 3>
+                                  : append_kernel<W4_KV_I8, 4>;
   }
+  cudaError_t e = launch_pdl(kernel, grid, kThreads, 0, st, 1, false, p);
   if (e != cudaSuccess) return cuda_fail(e, "launch kv_append");
   if (in_place) {
     e = launch_pdl(advance_kernel, dim3(static_cast<unsigned>(by_seq)), kThreads, 0, st, 1, false, p, lengths_out);

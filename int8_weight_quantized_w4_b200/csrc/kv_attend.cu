@@ -25,6 +25,7 @@ using namespace w4kv;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kMostUnits = 16;
+constexpr int kShortUnits = 4;
 constexpr int kGatherCtas = 16;  // CTAs an SM that the weights are shared out for
 constexpr int kMaxLaneVecs = 2;  // float4s of a lane: 32 x 4 x 2 = 256, the largest head_dim
 
@@ -165,7 +166,8 @@ __global__ void __launch_bounds__(kJoinThreads) behind_kernel(const AttendParams
 struct Layout {
   AttendKernel kernel;
   int32_t chunks;
-  unsigned ranks;  // CTAs of an item's cluster; 0: runs of units, and a join
+  unsigned ranks;  // CTAs of an item's cluster; 0: not so
+  bool warps;      // an item a warp; neither: runs of units, and a join
   unsigned ctas;
   int64_t part_stride;
   size_t meta, lse2, scores, bytes;  // offsets, and the total
@@ -182,11 +184,12 @@ AttendKernel choose(const w4kv::View& c, int type, int32_t group) {
   }
 }
 
-// CTAs of a kernel that an SM holds (asked once for each kernel).
-w4_status resident(const AttendKernel& k, int* out) {
+// CTAs of a kernel that an SM holds (asked once for each kernel), in runs of
+// units and in warps' items.
+w4_status resident(const AttendKernel& k, int* out, int* warp_out) {
   struct Known {
     const void* fn;
-    int n;
+    int n, warp_n;
   };
   static thread_local Known known[16] = {};
   static thread_local int next = 0;
@@ -194,20 +197,26 @@ w4_status resident(const AttendKernel& k, int* out) {
   for (const Known& e : known)
     if (e.fn == fn) {
       *out = e.n;
+      *warp_out = e.warp_n;
       return W4_OK;
     }
-  int n = 0;
-  cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
-  if (e != cudaSuccess) return w4host::cuda_fail(e, "kv_attend shared memory");
-  e = cudaFuncSetAttribute(k.item_fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
+  const auto allow = [](void (*f)(const AttendParams), size_t smem) {
+    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  };
+  cudaError_t e = allow(k.fn, k.smem);
+  if (e == cudaSuccess) e = allow(k.item_fn, k.smem);
+  if (e == cudaSuccess) e = allow(k.warp_fn, k.warp_smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k.item_fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return w4host::cuda_fail(e, "kv_attend cluster size");
+  if (e != cudaSuccess) return w4host::cuda_fail(e, "kv_attend kernel attributes");
+  int n = 0, warp_n = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k.fn, kAttendThreads, k.smem);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&warp_n, k.warp_fn, kAttendThreads, k.warp_smem);
   if (e != cudaSuccess) return w4host::cuda_fail(e, "kv_attend occupancy");
-  if (n < 1) return w4host::fail(W4_ERR_CUDA, "kv_attend: no CTA fits an SM");
-  known[next] = {fn, n};
+  if (n < 1 || warp_n < 1) return w4host::fail(W4_ERR_CUDA, "kv_attend: no CTA fits an SM");
+  known[next] = {fn, n, warp_n};
   next = (next + 1) % 16;
   *out = n;
+  *warp_out = warp_n;
   return W4_OK;
 }
 
@@ -216,8 +225,8 @@ w4_status lay_out(const w4kv::View& c, int type, int64_t q_heads, bool with_acc,
   Layout L = {};
   L.kernel = choose(c, type, group);
   L.chunks = (group + L.kernel.rows - 1) / L.kernel.rows;
-  int per_sm = 0;
-  const w4_status rc = resident(L.kernel, &per_sm);
+  int per_sm = 0, warp_per_sm = 0;
+  const w4_status rc = resident(L.kernel, &per_sm, &warp_per_sm);
   if (rc != W4_OK) return rc;
   const int64_t items = int64_t(c.seqs) * c.heads * L.chunks;
   const int64_t most = items * ((c.capacity + L.kernel.unit - 1) / L.kernel.unit + L.kernel.over);
@@ -230,8 +239,11 @@ w4_status lay_out(const w4kv::View& c, int type, int64_t q_heads, bool with_acc,
   unsigned ranks = 16;
   while (ranks > 1 && (items * ranks > wave || ranks / 2 >= units)) ranks /= 2;
   L.ranks = items * ranks <= wave && units <= int64_t(kMostUnits) * ranks ? ranks : 0;
-  if (L.ranks != 0) {
-    L.ctas = static_cast<unsigned>(items * ranks);
+  // More items than a wave of CTAs, and all of them short.
+  L.warps = L.ranks == 0 && items > wave && c.capacity <= kShortUnits * L.kernel.unit;
+  if (L.ranks != 0 || L.warps) {
+    const int64_t by_warp = std::min((items + kWarps - 1) / kWarps, int64_t(warp_per_sm) * sms);
+    L.ctas = static_cast<unsigned>(L.warps ? by_warp : items * ranks);
     L.lse2 = 0;
     L.scores = with_acc ? round256(static_cast<size_t>(c.seqs) * q_heads * 4) : 0;
     L.bytes = L.scores + (with_acc ? static_cast<size_t>(c.seqs) * q_heads * c.capacity * 4 : 0);
@@ -320,12 +332,13 @@ extern "C" w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, i
   p.chunks = L.chunks;
   p.err = di->err;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(L.ranks != 0 ? L.kernel.item_fn : L.kernel.fn, dim3(L.ctas), kAttendThreads, L.kernel.smem,
-                             st, L.ranks != 0 ? L.ranks : 1, true, p);
+  cudaError_t e = launch_pdl(L.ranks != 0 ? L.kernel.item_fn : (L.warps ? L.kernel.warp_fn : L.kernel.fn), dim3(L.ctas),
+                             kAttendThreads, L.warps ? L.kernel.warp_smem : L.kernel.smem, st,
+                             L.ranks != 0 ? L.ranks : 1, true, p);
   if (e != cudaSuccess) return cuda_fail(e, "launch kv_attend");
   int64_t joins = 0, gathers = 0, per_seq = 1;
   int wpr = 1;
-  if (L.ranks == 0) {
+  if (L.ranks == 0 && !L.warps) {
     const int64_t rows = c->seqs * q_heads;
     wpr = rows <= int64_t(di->sms) * kJoinWarps ? kJoinWarps : 1;
     const int64_t rows_per_cta = kJoinWarps / wpr;

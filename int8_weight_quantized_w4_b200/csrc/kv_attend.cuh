@@ -20,7 +20,8 @@
 // in the order of the slots. So no result depends on timing, and nothing has
 // to be zero beforehand. Where one wave of clusters holds all items with a few
 // units for each CTA, an item is a cluster instead, and its CTAs join theirs
-// through shared memory: one launch, no workspace traffic.
+// through shared memory: one launch, no workspace traffic. And where there are
+// more items than that but all are short, each warp takes items of its own.
 //
 // Latency. Each warp feeds itself: its tiles of 4 to 16 slots follow one another
 // across the segments of its CTA's run, and while it works on one the next
@@ -215,6 +216,7 @@ template <int TS>
 struct Ahead {
   Walk w;
   int32_t b, h, tile, s1;
+  int32_t stride;  // slots to this warp's next tile
   bool live;
 
   __device__ __forceinline__ void open(const AttendParams& p, const Run& run) {
@@ -225,12 +227,23 @@ struct Ahead {
       b = s.b;
       h = s.h;
       s1 = s.s1;
+      stride = kWarps * TS;
       tile = s.s0 + static_cast<int32_t>(threadIdx.x >> 5) * TS;
     } while (tile >= s1);
   }
+  // One segment only: the first tile of warp `warp` of `team`.
+  __device__ __forceinline__ void only(const Segment& s, int warp, int team) {
+    w.left = 0;
+    b = s.b;
+    h = s.h;
+    s1 = s.s1;
+    stride = team * TS;
+    tile = s.s0 + warp * TS;
+    live = tile < s1;
+  }
   __device__ __forceinline__ void step(const AttendParams& p, const Run& run) {
     if (!live) return;
-    tile += kWarps * TS;
+    tile += stride;
     if (tile >= s1) open(p, run);
   }
 };
@@ -370,7 +383,7 @@ __device__ __forceinline__ void attend_runs(const AttendParams& p, uint8_t* smem
     if (!more) break;
     queries.store(sq);
     __syncthreads();
-    float* to = Body::segment(p, run, s, feed, sq, body);
+    float* to = Body::template segment<kWarps>(p, run, s, feed, sq, body);
     if ((threadIdx.x & 31) == 0) triple[threadIdx.x >> 5] = to;
     prev = s;
   }
@@ -403,18 +416,13 @@ __device__ __forceinline__ void attend_item(const AttendParams& p, uint8_t* smem
   s.s1 = min(n, lo + (to << p.unit_log));
   const Run run = {};  // not asked: the walk holds no further unit
   typename Body::Feed feed;
-  feed.ahead.w.left = 0;
-  feed.ahead.b = s.b;
-  feed.ahead.h = s.h;
-  feed.ahead.s1 = s.s1;
-  feed.ahead.tile = s.s0 + static_cast<int32_t>(threadIdx.x >> 5) * Body::TS;
-  feed.ahead.live = feed.ahead.tile < s.s1;
+  feed.ahead.only(s, threadIdx.x >> 5, kWarps);
   Queries<ROWS, Body::kWidth> queries;
   queries.fetch(p, s);
   feed.begin(p, run, smem + (threadIdx.x >> 5) * Body::Feed::kRing);
   queries.store(sq);
   __syncthreads();
-  float* own = Body::segment(p, run, s, feed, sq, body);
+  float* own = Body::template segment<kWarps>(p, run, s, feed, sq, body);
   if ((threadIdx.x & 31) == 0) triple[threadIdx.x >> 5] = own;
   __syncthreads();
   join_warps<ROWS>(p, s.ng, triple, [&](int g, int d, const Triple& x) {
@@ -434,6 +442,49 @@ __device__ __forceinline__ void attend_item(const AttendParams& p, uint8_t* smem
     write_out(p, s.b, s.q0 + g, d, x);
   }
   cluster.sync();  // no CTA leaves while its triple is read
+}
+
+// Short items, one after the other, by each warp.
+template <class Body, int ROWS>
+__device__ __forceinline__ void attend_warps(const AttendParams& p, uint8_t* smem) {
+  constexpr int kOwn = (Body::Feed::kRing + (ROWS * (Body::kWidth + 2) + Body::kBodyFloats) * 4 + 127) / 128 * 128;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint8_t* own = smem + warp * kOwn;
+  float* sq = reinterpret_cast<float*>(own + Body::Feed::kRing);
+  float* body = sq + ROWS * (Body::kWidth + 2);
+  const int32_t items = p.c.heads * p.chunks, all = p.c.seqs * items, D = p.c.dim, quads = D / 4;
+  const Run run = {};
+  for (int32_t item = blockIdx.x * kWarps + warp; item < all; item += gridDim.x * kWarps) {
+    Segment s = {};
+    s.b = item / items;
+    s.item = item - s.b * items;
+    s.h = p.chunks == 1 ? s.item : s.item / p.chunks;
+    const int32_t g0 = (s.item - s.h * p.chunks) * p.rows;
+    s.q0 = s.h * p.group + g0;
+    s.ng = min(p.rows, p.group - g0);
+    attended(p, s.b, s.s0, s.s1);
+    typename Body::Feed feed;
+    feed.ahead.only(s, 0, 1);
+    feed.begin(p, run, own);
+    const float* q = p.q + s.b * p.ldq + int64_t(s.q0) * D;
+    for (int i = lane; i < ROWS * Body::kWidth / 4; i += 32) {
+      const int g = i / (Body::kWidth / 4), d = i % (Body::kWidth / 4) * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (g < s.ng && d < D) {
+        const float* from = q + g * D + d;
+        x = p.q_vec ? *reinterpret_cast<const float4*>(from) : make_float4(from[0], from[1], from[2], from[3]);
+      }
+      *reinterpret_cast<float4*>(sq + 4 * i) = x;
+    }
+    __syncwarp();
+    const float* t = Body::template segment<1>(p, run, s, feed, sq, body);
+    __syncwarp();
+    for (int i = lane; i < s.ng * quads; i += 32) {
+      const int g = i / quads, d = 4 * (i - g * quads);
+      write_out(p, s.b, s.q0 + g, d, stored(t, ROWS, D, g, d));
+    }
+    __syncwarp();  // the next item's first tile may come to where the triple lies
+  }
 }
 
 // ---------------------------------------------------------------- plain lanes
@@ -597,10 +648,11 @@ struct PlainLanes {
   static constexpr int kMinCtas = GT * VPL * EPV <= 16 ? 5 : (GT * VPL * EPV <= 32 ? 4 : (GT * VPL * EPV <= 64 ? 3 : 2));
   using Feed = Ring<TYPE, TS, LPR, VPL, LPR * VPL, false, 2, GT * (kWidth + 2)>;
 
-  // The warp's triple of the segment, and where it has been put.
+  // The warp's triple of its share (one of TEAM) of the segment: where it has been put.
+  template <int TEAM>
   __device__ static __forceinline__ float* segment(const AttendParams& p, const Run& run, const Segment& seg, Feed& feed,
                                                    const float* sq, float*) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR, rg = lane / LPR;
+    const int lane = threadIdx.x & 31, warp = TEAM == 1 ? 0 : threadIdx.x >> 5, sub = lane % LPR, rg = lane / LPR;
     const int D = p.c.dim, n16 = D / EPV;
     constexpr int W = kWidth;
     const int32_t s1 = seg.s1;
@@ -613,7 +665,7 @@ struct PlainLanes {
       for (int d = 0; d < VPL * EPV; ++d) a[g][d] = 0.f;
     }
 #pragma unroll 1
-    for (int32_t t = seg.s0 + warp * TS; t < s1; t += kWarps * TS) {
+    for (int32_t t = seg.s0 + warp * TS; t < s1; t += TEAM * TS) {
       uint32_t held;
       const uint8_t* stage = feed.take(p, run, held);
       const uint8_t* mine = stage + Feed::place(rg, sub);
@@ -754,6 +806,14 @@ __global__ void __launch_bounds__(kAttendThreads, Body::kMinCtas) attend_kernel(
 }
 
 template <class Body, int ROWS>
+__global__ void __launch_bounds__(kAttendThreads, Body::kMinCtas) attend_warp_kernel(const AttendParams p) {
+  extern __shared__ __align__(128) uint8_t attend_smem[];
+  pdl_launch_dependents();
+  pdl_wait();
+  attend_warps<Body, ROWS>(p, attend_smem);
+}
+
+template <class Body, int ROWS>
 __global__ void __launch_bounds__(kAttendThreads, Body::kMinCtas) attend_item_kernel(const AttendParams p) {
   extern __shared__ __align__(128) uint8_t attend_smem[];
   pdl_launch_dependents();
@@ -765,27 +825,38 @@ __global__ void __launch_bounds__(kAttendThreads, Body::kMinCtas) attend_item_ke
 struct AttendKernel {
   void (*fn)(const AttendParams);       // runs of units
   void (*item_fn)(const AttendParams);  // an item a cluster
+  void (*warp_fn)(const AttendParams);  // an item a warp
   int rows;         // query heads of an item
   int unit;         // slots of a unit
   int over;         // an item's own cost, in units
-  size_t smem;      // bytes of shared memory
+  size_t smem;      // bytes of shared memory; of warp_fn's
+  size_t warp_smem;
 };
 
 template <class Body, int ROWS>
 AttendKernel attend_kernel_of() {
-  return {attend_kernel<Body, ROWS>, attend_item_kernel<Body, ROWS>, ROWS, kWarps * Body::TS, Body::kOver,
-          size_t(kWarps) * Body::Feed::kRing + (size_t(ROWS) * (Body::kWidth + 2) + Body::kBodyFloats) * 4};
+  return {attend_kernel<Body, ROWS>, attend_item_kernel<Body, ROWS>, attend_warp_kernel<Body, ROWS>, ROWS, kWarps * Body::TS, Body::kOver,
+          size_t(kWarps) * Body::Feed::kRing + (size_t(ROWS) * (Body::kWidth + 2) + Body::kBodyFloats) * 4,
+          size_t(kWarps) *
+              ((Body::Feed::kRing + (ROWS * (Body::kWidth + 2) + Body::kBodyFloats) * 4 + 127) / 128 * 128)};
 }
 
 // The kernel for a call of this element type (one translation unit a type).
 template <int TYPE>
 AttendKernel attend_kernel_for(int32_t dim, int32_t group);
 
+// Query heads at once: up to 2, and for fp32, whose rows have no exact matrix
+// operands, 4, or 8 where their sums fit the registers.
 template <int TYPE, int LPR, int VPL>
 AttendKernel plain_kernel_for(int32_t group) {
   if (group == 1) return attend_kernel_of<PlainLanes<TYPE, LPR, VPL, 1>, 1>();
-  if (group == 2) return attend_kernel_of<PlainLanes<TYPE, LPR, VPL, 2>, 2>();
-  return attend_kernel_of<PlainLanes<TYPE, LPR, VPL, 4>, 4>();
+  if constexpr (TYPE == W4_KV_F32) {
+    if constexpr (VPL <= 2) {
+      if (group > 4) return attend_kernel_of<PlainLanes<TYPE, LPR, VPL, 8>, 8>();
+    }
+    if (group > 2) return attend_kernel_of<PlainLanes<TYPE, LPR, VPL, 4>, 4>();
+  }
+  return attend_kernel_of<PlainLanes<TYPE, LPR, VPL, 2>, 2>();
 }
 
 // The narrowest shape that holds a row's vectors.

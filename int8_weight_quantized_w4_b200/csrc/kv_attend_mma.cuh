@@ -97,7 +97,7 @@ struct MatrixLanes {
   static constexpr int VB = I8 && MAXD <= 64 ? 8 : 16;  // bytes of a value load
   static constexpr int VE = VB / E::kBytes;             // its elements
   static constexpr int NC = (MAXD / VE + 7) / 8;        // value vectors of a lane
-  static constexpr int NT = I8 ? 2 : 1;                 // 16 slots each, at once: int8's stages have room for two
+  static constexpr int NT = I8 && MAXD <= 128 ? 2 : 1;  // 16 slots each, at once: int8's stages have room for two
   static constexpr int TS = 16 * NT;
   static constexpr int kLift = 14;  // fp16 pieces: the exponent of the largest query, and of the largest weight
   static constexpr float kBelow = BF ? 0.f : kLift - kSlack;  // a new reference lies this far below the maximum
@@ -105,9 +105,9 @@ struct MatrixLanes {
   static constexpr int kWidth = MAXD;  // of a row of queries in shared memory
   static constexpr int kBodyFloats = kFrag;
   static constexpr int kOver = 3;  // beginning and ending a segment takes about 5 us, a unit 2 to 3 us
-  static constexpr int kMinCtas = 3;
-  static constexpr int CV = MAXD == 96 ? 3 : 1;         // copies: lanes of a row, vectors of a lane
-  static constexpr int CL = MAXD / EPV / CV;
+  static constexpr int kMinCtas = MAXD <= 128 ? 3 : (MAXD == 256 && !I8 ? 1 : 2);
+  static constexpr int CV = MAXD / EPV % 3 == 0 ? 3 : (MAXD / EPV == 32 ? 2 : 1);  // copies: vectors of a lane,
+  static constexpr int CL = MAXD / EPV / CV;                                       // lanes of a row
   using Feed = Ring<TYPE, TS, CL, CV, (MAXD / EPV + 7) / 8 * 8, true, 2, ROWS * (MAXD + 2)>;
   using VVec = typename std::conditional<VB == 16, uint4, uint2>::type;
 
@@ -116,25 +116,29 @@ struct MatrixLanes {
 
   // The queries as A operands in shared memory, in the order the lanes read
   // them; returns what this lane's head's scores are multiplied by for it.
+  template <int TEAM>
   __device__ static __forceinline__ float stage_queries(uint32_t* frag, const float* sq) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, warp = TEAM == 1 ? 0 : threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     float factor = 1.f, scale = 1.f;
     if constexpr (!BF) {
       // 2^(14 - e), 2^e the power below the largest |q| of each row; the scores take it back
 #pragma unroll
       for (int h = 0; h < ROWS; ++h) {
         uint32_t top = 0;
-        if (4 * lane < MAXD) {
-          const float4 x = *reinterpret_cast<const float4*>(sq + h * MAXD + 4 * lane);
-          top = max(max(__float_as_uint(fabsf(x.x)), __float_as_uint(fabsf(x.y))),
-                    max(__float_as_uint(fabsf(x.z)), __float_as_uint(fabsf(x.w))));
+#pragma unroll
+        for (int d = 0; d < MAXD; d += 128) {
+          if (d + 4 * lane < MAXD) {
+            const float4 x = *reinterpret_cast<const float4*>(sq + h * MAXD + d + 4 * lane);
+            top = max(top, max(max(__float_as_uint(fabsf(x.x)), __float_as_uint(fabsf(x.y))),
+                               max(__float_as_uint(fabsf(x.z)), __float_as_uint(fabsf(x.w)))));
+          }
         }
         top = __reduce_max_sync(0xffffffffu, top);
         if (h == g) factor = power_of_two(max(kLift + 1, min(253, static_cast<int>(top >> 23))) - 127 - kLift);
       }
       scale = 1.f / factor;
     }
-    for (int s = warp; s < SETS * STEPS; s += kWarps) {
+    for (int s = warp; s < SETS * STEPS; s += TEAM) {
       const int set = s / STEPS, st = s % STEPS;
       const int d = (t + 4 * (st / (EPV / 4))) * EPV + 4 * (st % (EPV / 4));
       uint32_t a[4];
@@ -155,7 +159,11 @@ struct MatrixLanes {
       }
       *reinterpret_cast<uint4*>(frag + (s * 32 + lane) * 4) = make_uint4(a[0], a[1], a[2], a[3]);
     }
-    __syncthreads();
+    if (TEAM == 1) {
+      __syncwarp();
+    } else {
+      __syncthreads();
+    }
     return factor;
   }
 
@@ -168,21 +176,22 @@ struct MatrixLanes {
     return v;
   }
 
-  // The warp's triple of the segment, and where it has been put.
+  // The warp's triple of its share (one of TEAM) of the segment: where it has been put.
+  template <int TEAM>
   __device__ static __forceinline__ float* segment(const AttendParams& p, const Run& run, const Segment& seg, Feed& feed,
                                                    const float* sq, float* body) {
     uint32_t* frag = reinterpret_cast<uint32_t*>(body);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, warp = TEAM == 1 ? 0 : threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int D = p.c.dim, head = g % ROWS;
     const int32_t s1 = seg.s1;
-    const float scale = stage_queries(frag, sq) * p.scale2;
+    const float scale = stage_queries<TEAM>(frag, sq) * p.scale2;
     float m = -INFINITY, l = 0.f;
     float acc[NC * VE][4];
 #pragma unroll
     for (int i = 0; i < NC * VE; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     int vexp = 1;  // int8: exponent field of the largest value scale so far; acc is in units of 2^(vexp - 127)
 #pragma unroll 1
-    for (int32_t tile = seg.s0 + warp * TS; tile < s1; tile += kWarps * TS) {
+    for (int32_t tile = seg.s0 + warp * TS; tile < s1; tile += TEAM * TS) {
       uint32_t held;
       const uint8_t* stage = feed.take(p, run, held);
       const float* scales = reinterpret_cast<const float*>(stage + Feed::kScales);
@@ -369,7 +378,9 @@ AttendKernel matrix_kernel_for(int32_t dim) {
   if constexpr (TYPE != W4_KV_I8) {
     if (dim <= 96) return attend_kernel_of<MatrixLanes<TYPE, ROWS, 96>, ROWS>();
   }
-  return attend_kernel_of<MatrixLanes<TYPE, ROWS, 128>, ROWS>();
+  if (dim <= 128) return attend_kernel_of<MatrixLanes<TYPE, ROWS, 128>, ROWS>();
+  if (dim <= 192) return attend_kernel_of<MatrixLanes<TYPE, ROWS, 192>, ROWS>();
+  return attend_kernel_of<MatrixLanes<TYPE, ROWS, 256>, ROWS>();
 }
 
 }  // namespace w4kv

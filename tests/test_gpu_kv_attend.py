@@ -67,7 +67,7 @@ def room_for(slots, page):
 @pytest.mark.parametrize("heads,group,dim,page", [
     (12, 1, 64, 16), (3, 1, 96, 7), (2, 2, 128, 32), (2, 3, 48, 5), (1, 4, 128, 64), (2, 8, 64, 16), (1, 5, 80, 1),
     (1, 16, 32, 3), (2, 7, 112, 33), (1, 1, 256, 16), (1, 9, 256, 20), (2, 1, 16, 4), (1, 4, 192, 8), (1, 6, 96, 16),
-    (1, 2, 160, 16), (1, 12, 128, 16),
+    (1, 2, 160, 16), (1, 12, 128, 16), (2, 3, 256, 16), (1, 8, 192, 7), (1, 5, 160, 16), (1, 4, 224, 16), (2, 8, 256, 5),
 ])
 def test_attend_matches_the_definition(kind, heads, group, dim, page, room):
     rng = np.random.default_rng(heads * 1000 + group * 100 + dim + page)
@@ -108,6 +108,20 @@ def test_attend_many_sequences(kind, room):
     cache, k, v = build(rng, kind, lengths, 2, 64, 16, max_pages=room_for(room, 16))
     q = rng.standard_normal((300, 4, 64)).astype(np.float32)
     check(cache, k, v, q, what="300 sequences")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("group,dim", [(1, 64), (2, 32), (3, 96), (8, 128), (16, 48), (5, 192)])
+def test_attend_many_short_items(kind, group, dim):
+    """More items than CTAs at once, all of them short: a warp for each."""
+    rng = np.random.default_rng(group * 100 + dim)
+    heads, n = 3, 400
+    lengths = [int(x) for x in rng.integers(0, 50, n)]
+    lengths[0] = lengths[1] = lengths[-1] = 0
+    cache, k, v = build(rng, kind, lengths, heads, dim, 16, max_pages=4)
+    q = rng.standard_normal((n, heads * group, dim)).astype(np.float32)
+    check(cache, k, v, q, with_acc=True, strided=True, what=f"short {kind} {group}x{dim}")
+    check(cache, k, v, q, window=9, what=f"short {kind} {group}x{dim} window")
 
 
 @pytest.mark.parametrize("room", ROOMS)

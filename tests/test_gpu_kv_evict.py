@@ -90,7 +90,7 @@ def test_evict_negative_infinite_and_nan_weights():
 
 
 @pytest.mark.parametrize("in_place", [False, True])
-@pytest.mark.parametrize("n,keep", [(20000, 5000), (70001, 69000), (9000, 1)])
+@pytest.mark.parametrize("n,keep", [(20000, 5000), (70001, 69000), (9000, 1), (150003, 40001)])
 def test_evict_one_long_sequence(in_place, n, keep):
     """Lengths that a cluster of CTAs shares."""
     run("bfloat16", [n], keep, keep // 10, heads=1, dim=32, in_place=in_place, seed=n)

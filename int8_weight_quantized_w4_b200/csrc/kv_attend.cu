@@ -26,6 +26,7 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kMostUnits = 16;
 constexpr int kShortUnits = 4;
+constexpr int kLeastSlots = 64;  // of a CTA in runs: fewer cost more to join than they save
 constexpr int kGatherCtas = 16;  // CTAs an SM that the weights are shared out for
 constexpr int kMaxLaneVecs = 2;  // float4s of a lane: 32 x 4 x 2 = 256, the largest head_dim
 
@@ -88,24 +89,40 @@ __device__ __forceinline__ void join_heads(const AttendParams& p, int wpr) {
     if (lane + 32 * j < vecs) write_out(p, b, qh, 4 * (lane + 32 * j), x[j]);
 }
 
-// A query head's log sum to base 2: as the attention kernel wrote it, or from
-// the partials, so that the weights need not wait for the join. -Inf: every
-// attended score is -Inf, and weighs nothing.
-__device__ __forceinline__ float lse2_of(const AttendParams& p, int32_t b, int32_t qh, bool runs) {
-  if (runs) {
-    int g;
-    const int2 meta = meta_of(p, b, qh, &g);
-    if (meta.y != 1) {
-      Triple x = no_slots();
+// The query heads' log sums to base 2, 32 heads at a time by 8 lanes each: as
+// the attention kernel wrote them, or from the partials, so that the weights
+// need not wait for the join. -Inf: every attended score is -Inf, and weighs
+// nothing.
+__device__ __forceinline__ void log_sums(const AttendParams& p, int32_t b, int32_t q0, int heads, bool runs, float* z) {
+  const int sub = threadIdx.x % 8;
+  for (int i0 = 0; i0 < heads; i0 += kJoinThreads / 8) {
+    const int i = i0 + threadIdx.x / 8;
+    const bool live = i < heads;
+    const int32_t qh = q0 + (live ? i : 0);
+    Triple x = no_slots();
+    int2 meta = make_int2(0, 1);
+    if (runs) {
+      int g;
+      meta = meta_of(p, b, qh, &g);
+      if (meta.y != 1) {
 #pragma unroll 4
-      for (int32_t i = 0; i < meta.y; ++i) {
-        const float* part = partial(p, meta, i) + p.rows * p.c.dim;
-        join(x, {make_float4(0.f, 0.f, 0.f, 0.f), part[g], part[p.rows + g]});
+        for (int32_t k = sub; k < meta.y; k += 8) {
+          const float* part = partial(p, meta, k) + p.rows * p.c.dim;
+          join(x, {make_float4(0.f, 0.f, 0.f, 0.f), part[g], part[p.rows + g]});
+        }
       }
-      return x.l == 0.f ? -INFINITY : x.m + log2f(x.l);
     }
+#pragma unroll
+    for (int o = 1; o < 8; o *= 2) {
+      const float m = __shfl_xor_sync(0xffffffffu, x.m, o), l = __shfl_xor_sync(0xffffffffu, x.l, o);
+      // the lower lane's first: both sides the same sum
+      Triple y = {x.a, sub & o ? m : x.m, sub & o ? l : x.l};
+      join(y, {x.a, sub & o ? x.m : m, sub & o ? x.l : l});
+      x = y;
+    }
+    if (live && sub == 0)
+      z[i] = meta.y == 1 ? p.lse2[int64_t(b) * p.c.heads * p.group + qh] : (x.l == 0.f ? -INFINITY : x.m + log2f(x.l));
   }
-  return p.lse2[int64_t(b) * p.c.heads * p.group + qh];
 }
 
 // acc[b, j] += sum over the query heads of 2^(x - lse2). A warp takes 32 slots
@@ -125,7 +142,7 @@ __device__ __forceinline__ void gather_weights(const AttendParams& p, int block,
       const int heads = min(kJoinThreads, q_heads - q0);
       if (q_heads > kJoinThreads || j0 == lo + int64_t(block) * 32) {
         __syncthreads();
-        if (threadIdx.x < heads) z[threadIdx.x] = lse2_of(p, b, q0 + threadIdx.x, runs);
+        log_sums(p, b, q0, heads, runs, z);
         __syncthreads();
       }
       const float* x = p.scores + (int64_t(b) * q_heads + q0) * p.c.capacity + j;
@@ -327,6 +344,7 @@ extern "C" w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, i
   p.group = static_cast<int32_t>(q_heads / c->kv_heads);
   p.rows = L.kernel.rows;
   p.over = L.kernel.over;
+  p.least = std::max(1, kLeastSlots / L.kernel.unit);
   while ((1 << p.unit_log) < L.kernel.unit) ++p.unit_log;
   p.q_vec = (bits(q) & 15) == 0 && (c->seqs <= 1 || ldq % 4 == 0);
   p.chunks = L.chunks;

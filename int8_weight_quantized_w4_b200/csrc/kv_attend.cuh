@@ -59,6 +59,7 @@ struct AttendParams {
   int32_t group, rows, chunks;  // query heads of a key-value head, of an item, items of a key-value head
   int32_t unit_log;             // slots of a unit: a tile for each warp
   int32_t over;                 // an item's own cost, in units
+  int32_t least;                // units that a CTA takes at least
   int32_t q_vec;                // the rows of q are 16-byte aligned
   ErrorWord* err;
 };
@@ -146,7 +147,8 @@ __device__ inline bool find_run(const AttendParams& p, Walk& w, Run& run, int32_
     up += before;
     if (b0 == 0) {
       if (p.c.seqs <= kAttendThreads) sum = all;
-      const int32_t total = sum * items, ctas = min(total, static_cast<int32_t>(gridDim.x)), c = blockIdx.x;
+      const int32_t total = sum * items, c = blockIdx.x;
+      const int32_t ctas = max(min(total, 1), min(total / p.least, static_cast<int32_t>(gridDim.x)));
       if (c >= ctas) return false;
       const int32_t share = total / ctas, extra = total - share * ctas;
       u = c * share + min(c, extra);
@@ -851,7 +853,7 @@ template <int TYPE, int LPR, int VPL>
 AttendKernel plain_kernel_for(int32_t group) {
   if (group == 1) return attend_kernel_of<PlainLanes<TYPE, LPR, VPL, 1>, 1>();
   if constexpr (TYPE == W4_KV_F32) {
-    if constexpr (VPL <= 2) {
+    if constexpr (VPL <= 4) {
       if (group > 4) return attend_kernel_of<PlainLanes<TYPE, LPR, VPL, 8>, 8>();
     }
     if (group > 2) return attend_kernel_of<PlainLanes<TYPE, LPR, VPL, 4>, 4>();

@@ -550,7 +550,8 @@ typedef enum w4_kv_type { W4_KV_F32 = 0, W4_KV_F16 = 1, W4_KV_BF16 = 2, W4_KV_I8
  *   page_stride elements apart (page_stride >= kv_heads * page_size *
  *   head_dim, a multiple of head_dim; num_pages * page_stride is below 2^32
  *   rows of head_dim elements); 16-byte aligned. head_dim is a multiple of 16,
- *   at most 256; page_size is any number from 1 to 65536.
+ *   at most 256; page_size is any number from 1 to 65536, kv_heads from 1 to
+ *   4096; there are at most 65535 sequences.
  * - k_scales, v_scales: W4_KV_I8 only (NULL otherwise): fp32 [num_pages]
  *   [kv_heads][page_size], packed, 4-byte aligned.
  * - page_table: int32, row b (at b * ldp) names the pages of sequence b in
@@ -589,8 +590,9 @@ typedef struct kv_cache {
  * rows, say), 4-byte aligned.
  * - cu_tokens: int32 [seqs + 1] on the device, ascending: rows cu_tokens[b] ..
  *   cu_tokens[b + 1] - 1 go to sequence b, the first to slot lengths[b].
- *   Rows outside every sequence are not read. NULL: one row for each
- *   sequence (tokens == seqs).
+ *   Rows of no sequence are left out. An entry below the one before it, or
+ *   outside 0 .. tokens, records W4_ERR_VALUE; rows that are not there do not
+ *   count. NULL: one row for each sequence (tokens == seqs).
  * - lengths_out: int32 [seqs], lengths[b] + the rows given (the capacity at
  *   most). It may be the cache's own lengths (they advance in place) or
  *   memory apart from them. Rows beyond the capacity are not written and

@@ -93,12 +93,13 @@ struct AppendParams {
   ErrorWord* err;
 };
 
-// Rows of sequence b, by cu_tokens (one each without it).
+// Rows of sequence b, by cu_tokens (one each without it), of those there are.
 __device__ __forceinline__ int32_t rows_of(const AppendParams& p, int32_t b) {
   if (p.cu == nullptr) return 1;
-  const int64_t n = int64_t(p.cu[b + 1]) - p.cu[b];
-  if (n < 0) w4dev::record_error(p.err, W4_ERR_VALUE, w4dev::K_KV_APPEND, b);
-  return n < 0 ? 0 : static_cast<int32_t>(n > 0x3fffffff ? 0x3fffffff : n);
+  const int64_t from = p.cu[b], to = p.cu[b + 1];
+  if (from < 0 || to < from || to > p.tokens) w4dev::record_error(p.err, W4_ERR_VALUE, w4dev::K_KV_APPEND, b);
+  const int64_t n = min(to, p.tokens) - max(from, int64_t(0));
+  return n < 0 ? 0 : static_cast<int32_t>(min(n, int64_t(0x3fffffff)));
 }
 
 __device__ __forceinline__ int32_t advanced(const AppendParams& p, int32_t b) {
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
   if (p.cu != nullptr) {
     b = sequence_of(p, t);
     if (b >= c.seqs || p.cu[b] > t || p.cu[b + 1] <= t) return;  // a row of no sequence
-    const int64_t at = held_length(c, b, p.err, w4dev::K_KV_APPEND) + (t - p.cu[b]);
+    const int64_t at = held_length(c, b, p.err, w4dev::K_KV_APPEND) + (t - max(p.cu[b], 0));
     slot = static_cast<int32_t>(at < c.capacity ? at : c.capacity);
   }
   if (slot >= c.capacity) {

@@ -201,18 +201,18 @@ AttendKernel choose(const w4kv::View& c, int type, int32_t group) {
   }
 }
 
-// CTAs of a kernel that an SM holds (asked once for each kernel), in runs of
-// units and in warps' items.
-w4_status resident(const AttendKernel& k, int* out, int* warp_out) {
+// CTAs of a kernel that an SM holds (asked once for each kernel and device), in
+// runs of units and in warps' items.
+w4_status resident(const AttendKernel& k, int dev, int* out, int* warp_out) {
   struct Known {
     const void* fn;
-    int n, warp_n;
+    int dev, n, warp_n;
   };
   static thread_local Known known[16] = {};
   static thread_local int next = 0;
   const void* fn = reinterpret_cast<const void*>(k.fn);
   for (const Known& e : known)
-    if (e.fn == fn) {
+    if (e.fn == fn && e.dev == dev) {
       *out = e.n;
       *warp_out = e.warp_n;
       return W4_OK;
@@ -230,20 +230,22 @@ w4_status resident(const AttendKernel& k, int* out, int* warp_out) {
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&warp_n, k.warp_fn, kAttendThreads, k.warp_smem);
   if (e != cudaSuccess) return w4host::cuda_fail(e, "kv_attend occupancy");
   if (n < 1 || warp_n < 1) return w4host::fail(W4_ERR_CUDA, "kv_attend: no CTA fits an SM");
-  known[next] = {fn, n, warp_n};
+  known[next] = {fn, dev, n, warp_n};
   next = (next + 1) % 16;
   *out = n;
   *warp_out = warp_n;
   return W4_OK;
 }
 
-w4_status lay_out(const w4kv::View& c, int type, int64_t q_heads, bool with_acc, int sms, Layout* out) {
+w4_status lay_out(const w4kv::View& c, int type, int64_t q_heads, bool with_acc, const w4host::DeviceInfo& di,
+                  Layout* out) {
+  const int sms = di.sms;
   const int32_t group = static_cast<int32_t>(q_heads / c.heads);
   Layout L = {};
   L.kernel = choose(c, type, group);
   L.chunks = (group + L.kernel.rows - 1) / L.kernel.rows;
   int per_sm = 0, warp_per_sm = 0;
-  const w4_status rc = resident(L.kernel, &per_sm, &warp_per_sm);
+  const w4_status rc = resident(L.kernel, di.dev, &per_sm, &warp_per_sm);
   if (rc != W4_OK) return rc;
   const int64_t items = int64_t(c.seqs) * c.heads * L.chunks;
   const int64_t most = items * ((c.capacity + L.kernel.unit - 1) / L.kernel.unit + L.kernel.over);
@@ -253,7 +255,7 @@ w4_status lay_out(const w4kv::View& c, int type, int64_t q_heads, bool with_acc,
   // items, where it leaves a CTA kMostUnits units of a full sequence. One
   // 12 x 64 sequence of 1021 slots: 6.6 us against 9.1 us as runs and a join.
   const int64_t units = (c.capacity + L.kernel.unit - 1) / L.kernel.unit;
-  unsigned ranks = 16;
+  unsigned ranks = per_sm > 1 ? 16 : 8;  // wider than 8 is not given on every GPC where each CTA fills an SM
   while (ranks > 1 && (items * ranks > wave || ranks / 2 >= units)) ranks /= 2;
   L.ranks = items * ranks <= wave && units <= int64_t(kMostUnits) * ranks ? ranks : 0;
   // More items than a wave of CTAs, and all of them short.
@@ -291,7 +293,7 @@ extern "C" size_t kv_attend_workspace_size(const kv_cache* c, int64_t q_heads, i
   const DeviceInfo* di = nullptr;
   Layout L;
   if (check_cache(c, "cache", &v) != W4_OK || check_heads(v, q_heads) != W4_OK || c->seqs == 0 ||
-      current_device(&di) != W4_OK || lay_out(v, c->type, q_heads, with_acc != 0, di->sms, &L) != W4_OK)
+      current_device(&di) != W4_OK || lay_out(v, c->type, q_heads, with_acc != 0, *di, &L) != W4_OK)
     return 0;
   return L.bytes;
 }
@@ -320,7 +322,7 @@ extern "C" w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, i
   rc = current_device(&di);
   if (rc != W4_OK) return rc;
   Layout L;
-  rc = lay_out(p.c, c->type, q_heads, acc != nullptr, di->sms, &L);
+  rc = lay_out(p.c, c->type, q_heads, acc != nullptr, *di, &L);
   if (rc != W4_OK) return rc;
   if (L.bytes > 0 && (workspace == nullptr || workspace_bytes < L.bytes))
     return fail(W4_ERR_WORKSPACE, "kv_attend needs a workspace of %zu bytes, %zu given", L.bytes,

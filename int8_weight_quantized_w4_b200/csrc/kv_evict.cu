@@ -411,6 +411,13 @@ extern "C" w4_status kv_evict(const kv_cache* src, const float* acc, int64_t lda
   if (!in_place && src->max_pages > 0 && dst->max_pages > 0 &&
       (same_k || same_v || (src->k_scales != nullptr && (src->k_scales == dst->k_scales || src->v_scales == dst->v_scales))))
     return fail(W4_ERR_VALUE, "dst shares pages with src but is not the same cache");
+  const auto overlap = [](const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+  };
+  if (!in_place && !same_len &&
+      overlap(src->lengths, static_cast<size_t>(src->seqs) * 4, dst->lengths, static_cast<size_t>(src->seqs) * 4))
+    return fail(W4_ERR_VALUE, "dst's lengths overlap src's in part");
   if (!in_place && same_len) return fail(W4_ERR_VALUE, "dst shares its lengths with src but is not the same cache");
   if (dst->ldp == 0 && dst->seqs > 1 && dst->max_pages > 0)
     return fail(W4_ERR_VALUE, "sequences that share one row of pages (ldp == 0) cannot be evicted into");
@@ -419,6 +426,16 @@ extern "C" w4_status kv_evict(const kv_cache* src, const float* acc, int64_t lda
     return fail(W4_ERR_SHAPE, "ldacc and ldacc_out must be at least src's capacity of %d slots", int(p.c.capacity));
   if (acc == acc_out && ldacc != ldacc_out && src->seqs > 1)
     return fail(W4_ERR_SHAPE, "acc_out == acc needs ldacc_out == ldacc");
+  if (acc != acc_out) {
+    // rows apart from each other may lie between those of the other
+    const int64_t cap = p.c.capacity, rows = src->seqs - 1;
+    const size_t na = static_cast<size_t>(rows * ldacc + cap) * 4, nb = static_cast<size_t>(rows * ldacc_out + cap) * 4;
+    if (overlap(acc, rows > 0 ? na : cap * 4, acc_out, rows > 0 ? nb : cap * 4)) {
+      const int64_t off = (reinterpret_cast<intptr_t>(acc_out) - reinterpret_cast<intptr_t>(acc)) / 4;
+      const int64_t in = rows > 0 && ldacc == ldacc_out ? ((off % ldacc) + ldacc) % ldacc : 0;
+      if (in < cap || ldacc - in < cap) return fail(W4_ERR_VALUE, "acc_out overlaps acc in part");
+    }
+  }
   if (kept != nullptr && src->seqs > 1 && ldkept < keep) return fail(W4_ERR_SHAPE, "ldkept=%lld < keep", (long long)ldkept);
   const auto bits = [](const void* x) { return reinterpret_cast<uintptr_t>(x); };
   if ((bits(acc) | bits(acc_out) | bits(kept)) & 3) return fail(W4_ERR_ALIGN, "acc, acc_out and kept must be 4-byte aligned");

@@ -176,6 +176,21 @@ def test_append_beyond_the_capacity_and_broken_pages():
     assert error_status() == 8 and cache.lengths.tolist() == [3, 5]
 
 
+def test_append_counts_only_rows_that_are_there():
+    T = torch()
+    rng = np.random.default_rng(17)
+    cache, k, _ = build(rng, "float32", [30, 32], 2, 16, 16)
+    x = rng.standard_normal((4, 2, 16)).astype(np.float32)
+    d = T.from_numpy(x).cuda()
+    cache.lengths.copy_(T.tensor([3, 5], dtype=T.int32))
+    clear_error()
+    w4().kv_append(cache, d, d, cu_tokens=T.tensor([-2, 2, 100], dtype=T.int32, device="cuda"))
+    assert error_status() == 8 and cache.lengths.tolist() == [5, 7]
+    for b, n in enumerate((3, 5)):
+        gk, _ = read_rows(cache, b, n + 2)
+        assert np.array_equal(gk[:n], k[b][:n]) and np.array_equal(gk[n:], x[2 * b:2 * b + 2].astype(np.float64))
+
+
 def test_append_nothing():
     T = torch()
     rng = np.random.default_rng(18)

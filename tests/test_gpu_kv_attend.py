@@ -90,8 +90,11 @@ def test_attend_window(kind, window, room):
 
 @pytest.mark.parametrize("kind,heads,group,dim,n", [
     ("float32", 1, 1, 64, 20011), ("bfloat16", 2, 4, 128, 30000), ("int8", 1, 8, 128, 40003), ("float16", 1, 1, 96, 9001),
+    ("float16", 1, 8, 256, 1900), ("bfloat16", 1, 8, 256, 900), ("int8", 1, 4, 192, 3000), ("float32", 1, 8, 256, 800),
+    ("bfloat16", 1, 4, 128, 1000), ("int8", 2, 8, 64, 1024), ("float32", 1, 1, 256, 700),
 ])
 def test_attend_one_long_sequence_is_split_and_joined(kind, heads, group, dim, n):
+    """Of one sequence: 16 CTAs and more share an item."""
     rng = np.random.default_rng(n)
     cache, k, v = build(rng, kind, [n], heads, dim, 64)
     q = (rng.standard_normal((1, heads * group, dim)) * 2).astype(np.float32)

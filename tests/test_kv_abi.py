@@ -102,7 +102,8 @@ def test_attend_noops_need_no_device():
 @pytest.mark.parametrize("kw,status", [
     (dict(acc=0), 1), (dict(acc_out=0), 1), (dict(keep=-1), 8), (dict(recent=-1), 8), (dict(keep=1 << 31), 8),
     (dict(ldacc=63), 2), (dict(ldo=63), 2), (dict(acc=0x70002), 3), (dict(kept=0x90002, ldkept=8), 3),
-    (dict(kept=0x90000, ldkept=7), 2), (dict(acc_out=0x70000, ldo=65), 2),
+    (dict(kept=0x90000, ldkept=7), 2), (dict(acc_out=0x70000, ldo=65), 2), (dict(acc_out=0x70010), 8),
+    (dict(ldacc=127, ldo=127, acc_out=0x70000 + 64 * 4), 8),
 ])
 def test_evict_argument_errors(kw, status):
     d = desc(k=0x110000, v=0x120000, page_table=0x130000, lengths=0x140000)
@@ -111,7 +112,7 @@ def test_evict_argument_errors(kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(kv_heads=1), 2), (dict(head_dim=32), 2), (dict(page_size=8), 2), (dict(seqs=3), 2), (dict(type=1), 2),
-    (dict(k=0x10000), 8), (dict(v=0x20000), 8), (dict(lengths=0x40000), 8), (dict(ldp=0), 8),
+    (dict(k=0x10000), 8), (dict(v=0x20000), 8), (dict(lengths=0x40000), 8), (dict(lengths=0x40004), 8), (dict(ldp=0), 8),
 ])
 def test_evict_refuses_a_destination_that_does_not_fit(kw, status):
     a = dict(k=0x110000, v=0x120000, page_table=0x130000, lengths=0x140000)

@@ -661,7 +661,7 @@ class _On:
 def _elsewhere(device, stream) -> bool:
     """Whether a call has to be made inside _On: another stream than the
     current one is asked for, or the tensors' device is not the current one."""
-    return stream is not None or _torch().cuda.current_device() != device.index
+    return stream is not None or _torch()._C._cuda_getDevice() != device.index
 
 
 def kv_append(cache: KvCache, k, v, cu_tokens=None, lengths_out=None, stream=None):
@@ -681,7 +681,7 @@ def kv_append(cache: KvCache, k, v, cu_tokens=None, lengths_out=None, stream=Non
     if lengths_out is None:
         lengths_out = cache.lengths
     out = _vector(lengths_out, "lengths_out", torch.int32, cache.seqs, dev)
-    st = lib().kv_append(cache._ref, k.data_ptr(), ldk, v.data_ptr(), ldv, cu, n, out, _stream_handle(None))
+    st = lib().kv_append(cache._ref, k.data_ptr(), ldk, v.data_ptr(), ldv, cu, n, out, torch._C._cuda_getCurrentRawStream(dev.index))
     if st != 0:
         _check(st, "kv_append")
     return lengths_out
@@ -717,7 +717,7 @@ def kv_attend(q, cache: KvCache, scale: float | None = None, window: int = 0, ou
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     st = lib().kv_attend(cache._ref, q.data_ptr(), ldq, Hq, D ** -0.5 if scale is None else scale, window,
                          out.data_ptr(), ldo, _ptr(lse), _ptr(acc), ldacc, _ptr(ws),
-                         0 if ws is None else ws.numel() * ws.element_size(), _stream_handle(None))
+                         0 if ws is None else ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(dev.index))
     if st != 0:
         _check(st, "kv_attend")
     return out
@@ -751,7 +751,7 @@ def kv_evict(cache: KvCache, acc, keep: int, recent: int = 0, dst: KvCache | Non
     if ws is None and need:
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     st = lib().kv_evict(cache._ref, acc.data_ptr(), ld, keep, recent, dst._ref, acc_out.data_ptr(), ldo, _ptr(kept),
-                        ldk, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream_handle(None))
+                        ldk, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(dev.index))
     if st != 0:
         _check(st, "kv_evict")
     return dst.lengths
@@ -780,16 +780,17 @@ def token_logprobs(logits, tokens=None, top: int = 0, stream=None):
     ld = _matrix(logits, "logits", f32, M, V, dev)
     t = lp = tl = ti = 0
     logp = top_logp = top_ids = None
+    new = logits.new_empty
     if tokens is not None:
         t = _vector(tokens, "tokens", torch.int32, M, dev)
-        logp = torch.empty(M, dtype=f32, device=dev)
+        logp = new(M)
         lp = logp.data_ptr()
-    entropy = torch.empty(M, dtype=f32, device=dev)
+    entropy = new(M)
     if top > 0:
-        top_logp = torch.empty(M, top, dtype=f32, device=dev)
-        top_ids = torch.empty(M, top, dtype=torch.int32, device=dev)
+        top_logp = new(M, top)
+        top_ids = new(M, top, dtype=torch.int32)
         tl, ti = top_logp.data_ptr(), top_ids.data_ptr()
-    st = lib().token_logprobs(logits.data_ptr(), ld, t, M, V, top, lp, entropy.data_ptr(), tl, ti, _stream_handle(None))
+    st = lib().token_logprobs(logits.data_ptr(), ld, t, M, V, top, lp, entropy.data_ptr(), tl, ti, torch._C._cuda_getCurrentRawStream(dev.index))
     if st != 0:
         _check(st, "token_logprobs")
     return logp, entropy, top_logp, top_ids

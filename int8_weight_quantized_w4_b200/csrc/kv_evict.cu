@@ -1,13 +1,15 @@
 // kv_evict: cuts sequences to the slots that the attention has used most.
 //
-// select_kernel: one cluster per sequence. The threshold, the key of the last
-// slot that stays, is found exactly by four passes over 8-bit digits of an
-// order-preserving key (a histogram a pass, in shared memory, added up over
-// the cluster's CTAs); ties at the threshold stay from the lowest slot on. A
-// CTA reads its weights once and keeps them in shared memory, up to 16384; each
-// warp looks for the digit by itself, so that a pass has one barrier. Then each
-// thread places four neighbouring slots behind the kept ones before them: the
-// kept slots' list.
+// select_kernel: one cluster per sequence, whose CTAs hold its weights in shared
+// memory (up to 16640 each). The threshold, the key of the last slot that
+// stays, is found exactly by passes over the digits of an order-preserving key:
+// a histogram a pass, in shared memory, added up over the cluster's CTAs, and
+// searched from above. A digit has 12 bits (10 for short sequences, whose CTAs
+// are small), since a first one of 8 has a float's exponent in few bins, which
+// the adding threads wait for (16 sequences of up to 16000 slots: 24 us), and
+// two passes tell most thresholds apart. Ties at it stay from the lowest slot
+// on. Then each thread places four neighbouring slots behind the kept ones
+// before them: the kept slots' list.
 // move_kernel: the kept rows of keys, values and scales to the front. A CTA
 // looks up the places of its rows once and moves them for several heads, the
 // next head's rows on their way while one's are written. Row i comes from slot
@@ -24,13 +26,15 @@ namespace {
 using namespace w4kv;
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelThreads = 1024;
+constexpr int kSelSmall = 256;      // for sequences of up to kSmall slots: 9 us against 10 us with 1024 threads
+constexpr int kSmall = 2048;
 constexpr int kMaxRanks = 8;        // CTAs of a selecting cluster
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;
 constexpr int kMoveCtas = 4;        // CTAs an SM that the heads are shared out for
-constexpr int kHeld = 16384;        // weights that a selecting CTA keeps in shared memory
+constexpr int kShare = 4160;       // slots that a sequence grows by another CTA at
+constexpr int kHeld = 16640;        // weights that a selecting CTA keeps in shared memory
 
 struct EvictParams {
   View c, d;
@@ -53,10 +57,15 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p, int32_t room) {
+// A digit has a bin for each quarter of a thread.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) select_kernel(const EvictParams p, int32_t room) {
+  constexpr int kBits = THREADS == 1024 ? 12 : 10, kBins = 1 << kBits, kWarps = THREADS / 32;
+  static_assert(kBins == 4 * THREADS, "four digits a thread");
   extern __shared__ float weights[];  // of this CTA's slots, where there is room for them
-  __shared__ __align__(16) uint32_t hist[4][256];  // this CTA's counts, a pass each
-  __shared__ uint32_t total[256];     // the cluster's
+  __shared__ __align__(16) uint32_t hist[2][kBins];  // this CTA's counts: one pass fills one while others read the other
+  __shared__ uint32_t warp_sums[2][32];
+  __shared__ uint32_t picked[5];      // see below
   __shared__ uint32_t counts[2];      // slots of this CTA that stay for sure, and at the threshold
   __shared__ uint32_t warp_counts[2][32];
   pdl_launch_dependents();
@@ -82,7 +91,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     if (rank == 0 && tid == 0) w4dev::record_error(p.err, W4_ERR_VALUE, w4dev::K_KV_EVICT, b);
     fresh = p.d.capacity;
   }
-  const int32_t first = rank * kSelThreads + tid, step = ranks * kSelThreads;
+  const int32_t first = rank * THREADS + tid, step = ranks * THREADS;
   if (n <= p.keep) {
     for (int32_t i = first; i < fresh; i += step) {
       list[i] = i;
@@ -97,56 +106,51 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     const int32_t c0 = min(n, rank * chunk), c1 = min(n, c0 + chunk), m1 = min(c1, m);
     const bool held = chunk <= room;
     const auto weight = [&](int32_t i) { return held ? weights[i - c0] : acc[i]; };
-    for (int i = tid; i < 4 * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
+    *reinterpret_cast<uint4*>(&hist[0][4 * tid]) = make_uint4(0, 0, 0, 0);
     __syncthreads();
-#pragma unroll 4
-    for (int32_t i = c0 + tid; i < c1; i += kSelThreads) {
-      const float w = acc[i];
-      if (held) weights[i - c0] = w;
-      if (i < m) atomicAdd(&hist[0][weight_key(w) >> 24], 1u);
+    constexpr int kAhead = 8;
+    for (int32_t i0 = c0 + tid; i0 < c1; i0 += kAhead * THREADS) {
+      float w[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) w[j] = i0 + j * THREADS < c1 ? acc[i0 + j * THREADS] : 0.f;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int32_t i = i0 + j * THREADS;
+        if (i < c1 && held) weights[i - c0] = w[j];
+        if (i < m1) atomicAdd(&hist[0][weight_key(w[j]) >> (32 - kBits)], 1u);
+      }
     }
     sync_all();
     uint32_t prefix = 0, sure = 0, at_it = 0;  // the last two: this CTA's, of the slots that compete
     int low = 32;                              // `prefix` holds a key's bits from here on
-    for (int pass = 0; pass < 4 && !none; ++pass) {
-      const int shift = 24 - 8 * pass;
-      const uint32_t* mine = hist[pass];
+    for (int pass = 0; low > 0 && !none; ++pass) {
+      const int bits = min(low, kBits), shift = low - bits;
+      const uint32_t mask = (1u << bits) - 1u;
+      uint32_t* mine = hist[pass & 1];
       if (pass > 0) {
 #pragma unroll 4
-        for (int32_t i = c0 + tid; i < m1; i += kSelThreads) {
+        for (int32_t i = c0 + tid; i < m1; i += THREADS) {
           const uint32_t k = weight_key(weight(i));
-          if ((k >> (shift + 8)) == prefix) atomicAdd(&hist[pass][(k >> shift) & 255u], 1u);
+          if ((k >> low) == prefix) atomicAdd(&mine[(k >> shift) & mask], 1u);
         }
         sync_all();
       }
-      // Each warp finds the digit: lane l sums digits 8 l .. 8 l + 7, the largest digits first.
-      uint32_t t[8], c[8], own = 0, own_c = 0;
-#pragma unroll
-      for (int j = 0; j < 8; j += 4) {
-        const uint4 x = *reinterpret_cast<const uint4*>(mine + 8 * lane + j);
-        c[j] = x.x;
-        c[j + 1] = x.y;
-        c[j + 2] = x.z;
-        c[j + 3] = x.w;
-      }
+      // The digit: thread t sums digits 4 t .. 4 t + 3, of the cluster (t) and of this CTA (c).
+      const uint4 own4 = *reinterpret_cast<const uint4*>(mine + 4 * tid);
+      uint4 all4 = own4;
       if (ranks > 1) {
-        if (tid < 256) {
-          uint32_t sum = 0;
+        all4 = make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int r = 0; r < kMaxRanks; ++r)  // all on their way at once
-            if (r < ranks) sum += cluster.map_shared_rank(hist[pass], r)[tid];
-          total[tid] = sum;
+        for (int r = 0; r < kMaxRanks; ++r) {  // all on their way at once
+          if (r < ranks) {
+            const uint4 x = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(mine, r) + 4 * tid);
+            all4 = make_uint4(all4.x + x.x, all4.y + x.y, all4.z + x.z, all4.w + x.w);
+          }
         }
-        __syncthreads();
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = ranks > 1 ? total[8 * lane + j] : c[j];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        own += t[j];
-        own_c += c[j];
-      }
-      uint32_t above = own, above_c = own_c;
+      const uint32_t t[4] = {all4.x, all4.y, all4.z, all4.w}, c[4] = {own4.x, own4.y, own4.z, own4.w};
+      const uint32_t own = t[0] + t[1] + t[2] + t[3], own_c = c[0] + c[1] + c[2] + c[3];
+      uint32_t above = own, above_c = own_c;  // with the digits of the lanes above
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
         const uint32_t v = __shfl_down_sync(0xffffffffu, above, o), w = __shfl_down_sync(0xffffffffu, above_c, o);
@@ -155,31 +159,36 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
           above_c += w;
         }
       }
-      above -= own;  // in the digits of the lanes above
-      above_c -= own_c;
-      const bool here = above < want && want <= above + own;
-      const int at = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-      uint32_t digit = 0, left = 0, higher = 0, same = 0, all = 0;
-      if (here) {
+      if (lane == 0) {
+        warp_sums[0][warp] = above;
+        warp_sums[1][warp] = above_c;
+      }
+      // the other buffer's readers are behind the barrier above
+      *reinterpret_cast<uint4*>(&hist[(pass + 1) & 1][4 * tid]) = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+      above += __reduce_add_sync(0xffffffffu, lane > warp && lane < kWarps ? warp_sums[0][lane] : 0u) - own;
+      above_c += __reduce_add_sync(0xffffffffu, lane > warp && lane < kWarps ? warp_sums[1][lane] : 0u) - own_c;
+      if (above < want && want <= above + own) {
 #pragma unroll
-        for (int j = 7; j >= 0; --j) {
+        for (int j = 3; j >= 0; --j) {
           if (above < want && want <= above + t[j]) {
-            digit = 8 * lane + j;
-            left = want - above;
-            higher = above_c;
-            same = c[j];
-            all = t[j];
+            picked[0] = 4 * tid + j;
+            picked[1] = want - above;  // how many of the digit stay
+            picked[2] = t[j];          // of how many
+            picked[3] = above_c;       // this CTA's above it
+            picked[4] = c[j];          // and of it
           }
           above += t[j];
           above_c += c[j];
         }
       }
-      prefix = (prefix << 8) | __shfl_sync(0xffffffffu, digit, at);
-      want = __shfl_sync(0xffffffffu, left, at);
-      sure += __shfl_sync(0xffffffffu, higher, at);
-      at_it = __shfl_sync(0xffffffffu, same, at);
+      __syncthreads();
+      prefix = pass == 0 ? picked[0] : (prefix << bits) | picked[0];
+      want = picked[1];
+      sure += picked[3];
+      at_it = picked[4];
       low = shift;
-      if (__shfl_sync(0xffffffffu, all, at) == want) break;  // all of this digit stay: the rest decides nothing
+      if (picked[2] == want) break;  // all of this digit stay: the rest decides nothing
     }
     // `want` of the slots whose key begins with `prefix` stay, from the lowest on
     uint32_t sure_before = 0, at_before = 0;
@@ -199,7 +208,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     // fewer) they have all been read, and may be written over.
     float* out = held ? acc_out : kept_acc;
     int turn = 0;
-    for (int32_t t0 = c0; t0 < c1; t0 += 4 * kSelThreads, turn ^= 1) {
+    for (int32_t t0 = c0; t0 < c1; t0 += 4 * THREADS, turn ^= 1) {
       const int32_t i0 = t0 + 4 * tid;
       uint32_t is_sure = 0, is_at = 0;  // a bit for each of the four
       float w[4];
@@ -225,7 +234,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
       }
       if (lane == 31) warp_counts[turn][warp] = up;
       __syncthreads();
-      const uint32_t wc = lane < kSelWarps ? warp_counts[turn][lane] : 0u;
+      const uint32_t wc = lane < kWarps ? warp_counts[turn][lane] : 0u;
       const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? wc : 0u) + up - own;
       const uint32_t all = __reduce_add_sync(0xffffffffu, wc);
       uint32_t g = sure_before + (before & 0xFFFFu), e = at_before + (before >> 16);
@@ -359,11 +368,11 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 int64_t list_width(const View& c, int64_t keep) { return keep < c.capacity ? keep : c.capacity; }
 
-// CTAs of a sequence's cluster: up to 8 while the sequences alone do not fill
-// the SMs and a CTA's share is a thousand slots or more.
+// CTAs of a sequence's cluster: as many as hold its weights, up to 8, while the
+// sequences alone do not fill the SMs.
 unsigned select_ranks(const View& c, int sms) {
   unsigned ranks = 1;
-  while (ranks < kMaxRanks && int64_t(c.seqs) * ranks * 2 <= sms && c.capacity / (ranks * 2) >= 2 * kSelThreads) ranks *= 2;
+  while (ranks < kMaxRanks && int64_t(c.seqs) * ranks * 2 <= sms && (c.capacity + ranks - 1) / ranks + 4 > kShare) ranks *= 2;
   return ranks;
 }
 
@@ -471,11 +480,14 @@ extern "C" w4_status kv_evict(const kv_cache* src, const float* acc, int64_t lda
   const int32_t room = share <= kHeld ? static_cast<int32_t>(share) : kHeld;
   static thread_local int ready = -1;
   if (ready != di->dev) {
-    const cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4);
+    const cudaError_t e =
+        cudaFuncSetAttribute(select_kernel<kSelThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4);
     if (e != cudaSuccess) return cuda_fail(e, "kv_evict shared memory");
     ready = di->dev;
   }
-  cudaError_t e = launch_pdl(select_kernel, dim3(static_cast<unsigned>(src->seqs) * ranks), kSelThreads,
+  const bool small = p.c.capacity <= kSmall;
+  cudaError_t e = launch_pdl(small ? select_kernel<kSelSmall> : select_kernel<kSelThreads>,
+                             dim3(static_cast<unsigned>(src->seqs) * ranks), small ? kSelSmall : kSelThreads,
                              static_cast<size_t>(room) * 4, st, ranks, false, p, room);
   if (e != cudaSuccess) return cuda_fail(e, "launch kv_evict (select)");
   const int vecs = src->head_dim * elem_bytes(src->type) / 16;

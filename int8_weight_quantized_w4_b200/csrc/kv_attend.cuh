@@ -844,8 +844,10 @@ AttendKernel attend_kernel_of() {
 }
 
 // The kernel for a call of this element type (one translation unit a type).
+// brief: too few slots for the matrix body, whose staging of the queries is then
+// most of its time.
 template <int TYPE>
-AttendKernel attend_kernel_for(int32_t dim, int32_t group);
+AttendKernel attend_kernel_for(int32_t dim, int32_t group, bool brief);
 
 // Query heads at once: up to 2, and for fp32, whose rows have no exact matrix
 // operands, 4, or 8 where their sums fit the registers.

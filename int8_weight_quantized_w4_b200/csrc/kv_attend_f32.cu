@@ -4,7 +4,7 @@
 namespace w4kv {
 
 template <>
-AttendKernel attend_kernel_for<W4_KV_F32>(int32_t dim, int32_t group) {
+AttendKernel attend_kernel_for<W4_KV_F32>(int32_t dim, int32_t group, bool) {
   return plain_kernel_for<W4_KV_F32>(dim, group);
 }
 

@@ -114,6 +114,20 @@ def test_attend_many_sequences(kind, room):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("group,dim", [(1, 64), (3, 64), (8, 128), (5, 256), (13, 16)])
+def test_attend_few_slots(kind, group, dim):
+    """Sequences of at most one tile, in a small and in a large batch, and a
+    small batch of a few tiles: the plain lanes for any group."""
+    rng = np.random.default_rng(group + dim)
+    for n, most, heads in ((3, 16, 2), (500, 16, 3), (2, 250, 2)):
+        lengths = [int(x) for x in rng.integers(0, most + 1, n)]
+        lengths[-1] = most
+        cache, k, v = build(rng, kind, lengths, heads, dim, 16)
+        q = rng.standard_normal((n, heads * group, dim)).astype(np.float32)
+        check(cache, k, v, q, with_acc=n < 10, what=f"few slots {kind} {group}x{dim} {n}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("group,dim", [(1, 64), (2, 32), (3, 96), (8, 128), (16, 48), (5, 192)])
 def test_attend_many_short_items(kind, group, dim):
     """More items than CTAs at once, all of them short: a warp for each."""

@@ -636,6 +636,15 @@ def _matrix(t, name: str, dtype, n: int, width: int, device) -> int:
     return stride[0] if n > 1 else max(width, 1)
 
 
+def _room(ws, device) -> int:
+    """Bytes of a workspace."""
+    if ws is None:
+        return 0
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
+    return ws.numel() * ws.element_size()
+
+
 class _On:
     """Makes a tensor's device current, and `stream` if one is given: what is
     allocated inside belongs to the stream that the call runs on."""
@@ -681,7 +690,8 @@ def kv_append(cache: KvCache, k, v, cu_tokens=None, lengths_out=None, stream=Non
     if lengths_out is None:
         lengths_out = cache.lengths
     out = _vector(lengths_out, "lengths_out", torch.int32, cache.seqs, dev)
-    st = lib().kv_append(cache._ref, k.data_ptr(), ldk, v.data_ptr(), ldv, cu, n, out, torch._C._cuda_getCurrentRawStream(dev.index))
+    st = lib().kv_append(cache._ref, k.data_ptr(), ldk, v.data_ptr(), ldv, cu, n, out,
+                         torch._C._cuda_getCurrentRawStream(dev.index))
     if st != 0:
         _check(st, "kv_append")
     return lengths_out
@@ -716,8 +726,8 @@ def kv_attend(q, cache: KvCache, scale: float | None = None, window: int = 0, ou
     if ws is None and need:
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     st = lib().kv_attend(cache._ref, q.data_ptr(), ldq, Hq, D ** -0.5 if scale is None else scale, window,
-                         out.data_ptr(), ldo, _ptr(lse), _ptr(acc), ldacc, _ptr(ws),
-                         0 if ws is None else ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(dev.index))
+                         out.data_ptr(), ldo, _ptr(lse), _ptr(acc), ldacc, _ptr(ws), _room(ws, dev),
+                         torch._C._cuda_getCurrentRawStream(dev.index))
     if st != 0:
         _check(st, "kv_attend")
     return out
@@ -751,7 +761,7 @@ def kv_evict(cache: KvCache, acc, keep: int, recent: int = 0, dst: KvCache | Non
     if ws is None and need:
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     st = lib().kv_evict(cache._ref, acc.data_ptr(), ld, keep, recent, dst._ref, acc_out.data_ptr(), ldo, _ptr(kept),
-                        ldk, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(dev.index))
+                        ldk, _ptr(ws), _room(ws, dev), torch._C._cuda_getCurrentRawStream(dev.index))
     if st != 0:
         _check(st, "kv_evict")
     return dst.lengths
@@ -790,7 +800,8 @@ def token_logprobs(logits, tokens=None, top: int = 0, stream=None):
         top_logp = new(M, top)
         top_ids = new(M, top, dtype=torch.int32)
         tl, ti = top_logp.data_ptr(), top_ids.data_ptr()
-    st = lib().token_logprobs(logits.data_ptr(), ld, t, M, V, top, lp, entropy.data_ptr(), tl, ti, torch._C._cuda_getCurrentRawStream(dev.index))
+    st = lib().token_logprobs(logits.data_ptr(), ld, t, M, V, top, lp, entropy.data_ptr(), tl, ti,
+                              torch._C._cuda_getCurrentRawStream(dev.index))
     if st != 0:
         _check(st, "token_logprobs")
     return logp, entropy, top_logp, top_ids

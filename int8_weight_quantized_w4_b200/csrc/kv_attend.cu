@@ -313,7 +313,8 @@ extern "C" w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, i
   rc = check_heads(p.c, q_heads);
   if (rc != W4_OK) return rc;
   if (window < 0) return fail(W4_ERR_VALUE, "window=%lld is negative", (long long)window);
-  if (!(scale > -INFINITY && scale < INFINITY)) return fail(W4_ERR_VALUE, "scale is not finite");
+  p.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  if (!(p.scale2 > -INFINITY && p.scale2 < INFINITY)) return fail(W4_ERR_VALUE, "scale is not finite, or too large");
   if (c->seqs == 0) return W4_OK;
   if (q == nullptr || out == nullptr) return fail(W4_ERR_NULL, "q and out must not be NULL");
   if (c->seqs > 1 && (ldq < q_heads * c->head_dim || ldo < q_heads * c->head_dim))
@@ -347,7 +348,6 @@ extern "C" w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, i
   }
   p.part_stride = L.part_stride;
   p.window = window;
-  p.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.group = static_cast<int32_t>(q_heads / c->kv_heads);
   p.rows = L.kernel.rows;
   p.over = L.kernel.over;

@@ -349,3 +349,40 @@ def test_attend_refusals():
         w4().kv_attend(q, cache, acc=T.zeros((2, 47), device="cuda"))
     with pytest.raises(ValueError):
         w4().kv_attend(q, cache, out=T.zeros((2, 4, 64), device="cuda").half())
+
+
+def test_attend_workspace_refusals():
+    T = torch()
+    rng = np.random.default_rng(82)
+    cache, _, _ = build(rng, "float32", [40, 48], 2, 64, 16)
+    q, acc = T.zeros((2, 4, 64), device="cuda"), T.zeros((2, 48), device="cuda")
+    room = 1 << 20
+    for bad in (T.zeros(room, dtype=T.uint8), T.zeros(1, dtype=T.uint8, device="cuda").expand(room),
+                T.zeros(2 * room, dtype=T.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            w4().kv_attend(q, cache, acc=acc, ws=bad)
+        with pytest.raises(ValueError):
+            w4().kv_evict(cache, acc, 8, ws=bad)
+    own = T.full((room // 4,), float("nan"), device="cuda")
+    want = w4().kv_attend(q, cache, acc=T.zeros_like(acc))
+    assert T.equal(want, w4().kv_attend(q, cache, acc=acc, ws=own))
+
+
+@pytest.mark.parametrize("kind,group", [("float32", 1), ("bfloat16", 1), ("bfloat16", 4), ("float32", 8), ("int8", 8)])
+def test_attend_large_values(kind, group):
+    """Values of 2^96 are averaged without overflow, whatever the scores do."""
+    T = torch()
+    rng = np.random.default_rng(83)
+    n, heads, dim = 600, 2, 64
+    cache, _, _ = build(rng, kind, [n], heads, dim, 16)
+    k = T.randn((n, heads, dim), device="cuda", generator=T.Generator("cuda").manual_seed(5))
+    k *= T.linspace(0.1, 3.0, n, device="cuda")[:, None, None]  # maxima that keep rising
+    v = T.full((n, heads, dim), 2.0 ** 96, device="cuda")
+    cache.lengths.zero_()
+    w4().kv_append(cache, k, v, cu_tokens=T.tensor([0, n], dtype=T.int32, device="cuda"))
+    q = T.randn((1, heads * group, dim), device="cuda", generator=T.Generator("cuda").manual_seed(6))
+    out = w4().kv_attend(q, cache)
+    # all values are alike: what differs is the rounding of two sums of 600 terms of one sign (each
+    # term at most 600 x 2^-24 off in its sum), the pieces' 2^-21 and, for int8, one rounding of the scale
+    bound = 2 * n * 2.0 ** -24 + 2.0 ** -20
+    assert float((out / 2.0 ** 96 - 1).abs().max()) <= bound

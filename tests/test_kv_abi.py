@@ -85,7 +85,7 @@ def test_append_more_refusals_and_noops():
 
 @pytest.mark.parametrize("kw,status", [
     (dict(q=0), 1), (dict(out=0), 1), (dict(heads=3), 2), (dict(heads=0), 2), (dict(heads=-2), 2), (dict(ldq=255), 2),
-    (dict(ldo=255), 2), (dict(window=-1), 8), (dict(scale=float("inf")), 8), (dict(scale=float("nan")), 8),
+    (dict(ldo=255), 2), (dict(window=-1), 8), (dict(scale=float("inf")), 8), (dict(scale=float("nan")), 8), (dict(scale=3e38), 8),
     (dict(q=0x70002), 3), (dict(out=0x80001), 3), (dict(lse=0x90002), 3), (dict(acc=0x90002, ldacc=64), 3),
     (dict(acc=0x90000, ldacc=63), 2),
 ])

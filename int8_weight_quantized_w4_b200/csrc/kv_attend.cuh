@@ -10,12 +10,12 @@
 // freely and each is read once.
 //
 // Work. The slots of one (sequence, key-value head, chunk of query heads), an
-// item, are cut into units of 16 to 64, a tile for each warp. All units of all items, in that order, are
-// dealt to the CTAs in equal contiguous runs, by the lengths on the device: a
-// batch of unequal lengths, one long sequence and many short ones all load
-// every SM alike, and a CUDA graph stays valid while the lengths grow. An item
-// counts a unit or two more than it has, what beginning and ending it costs. A
-// CTA holds at most one item that began before its run and one that goes on
+// item, are cut into units of 16 to 128, a tile for each warp. All units of all
+// items, in that order, are dealt to the CTAs in equal contiguous runs, by the
+// lengths on the device: a batch of unequal lengths, one long sequence and many
+// short ones all load every SM alike, and a CUDA graph stays valid while the
+// lengths grow. An item counts one to three units more than it has, what
+// beginning and ending it costs. A CTA holds at most one item that began before its run and one that goes on
 // behind it; those leave (m, l, a) in the workspace and behind_kernel joins them
 // in the order of the slots. So no result depends on timing, and nothing has
 // to be zero beforehand. Where one wave of clusters holds all items with a few
@@ -23,11 +23,16 @@
 // through shared memory: one launch, no workspace traffic. And where there are
 // more items than that but all are short, each warp takes items of its own.
 //
-// Latency. Each warp feeds itself: its tiles of 4 to 16 slots follow one another
+// Latency. Each warp feeds itself: its tiles of 4 to 32 slots follow one another
 // across the segments of its CTA's run, and while it works on one the next
 // ones are on their way into its ring of stages in shared memory (cp.async,
 // which also writes the zeros of slots that are not there), whichever segments
 // they belong to; their entries of the page table were fetched a tile earlier.
+//
+// Measured, call after call: 131072 slots of 8 x 128 bf16 for 32 query heads
+// 91 us, 5.9 TB/s of keys and values (0.91 of what a plain copy moves); 48
+// sequences of up to 1024 slots, 12 x 64 bf16, 19 us (4.0 TB/s); one of 1021
+// slots, 12 x 64 fp32, 5.6 us, bound by its chain of reads.
 #pragma once
 
 #include <cooperative_groups.h>

@@ -22,6 +22,14 @@
 //   values: vectors g, g + 8 of slots 2t, 2t+1, 2t+8, 2t+9; byte permutes pair
 //           the slots, element j of all vectors makes one product's columns.
 // The scores' accumulators are then the A operand of the second product.
+//
+// Why not the larger matrix instructions: the rows of A are the query heads of
+// one key-value head, so a 128-row operand would be mostly zeros, and int8
+// codes have to pass the registers anyway. Rate is not what is short: on
+// 131072 slots of 8 x 128 bf16 for 32 heads the tensor pipe is busy a fifth of
+// the time and DRAM delivers 6.1 TB/s; int8 (32 sequences of up to 4096 slots,
+// 8 x 128 for 64 heads: 58 us, 3.4 TB/s) is held by the conversions' dependent
+// instructions at the 12 warps that an SM's registers hold.
 #pragma once
 
 #include "kv_attend.cuh"

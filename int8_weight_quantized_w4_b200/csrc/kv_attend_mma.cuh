@@ -242,14 +242,12 @@ struct MatrixLanes {
       float x[2 * NT][2];
       float top = -INFINITY;
 #pragma unroll
-      for (int n = 0; n < 2 * NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int slot = 8 * n + 2 * t + e;
-          float f = scale;
-          if constexpr (I8) f *= scales[slot];
-          x[n][e] = joined(c[n][e], c[n][2 + e]) * f;
-        }
+      for (int n = 0; n < 2 * NT; ++n) {
+        float2 f = make_float2(1.f, 1.f);
+        if constexpr (I8) f = *reinterpret_cast<const float2*>(scales + 8 * n + 2 * t);
+        x[n][0] = joined(c[n][0], c[n][2]) * (scale * f.x);
+        x[n][1] = joined(c[n][1], c[n][3]) * (scale * f.y);
+      }
       if (held != Feed::kAll) {
 #pragma unroll
         for (int n = 0; n < 2 * NT; ++n)
@@ -300,13 +298,16 @@ struct MatrixLanes {
       }
       const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-      for (int n = 0; n < 2 * NT; ++n)
+      for (int n = 0; n < 2 * NT; ++n) {
+        float2 f = make_float2(1.f, 1.f);
+        if constexpr (I8) f = *reinterpret_cast<const float2*>(scales + TS + 8 * n + 2 * t);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           x[n][e] = ex2(x[n][e] - ref);
           l += x[n][e];
-          if constexpr (I8) x[n][e] *= scales[TS + 8 * n + 2 * t + e] * unit;
+          if constexpr (I8) x[n][e] *= (e == 0 ? f.x : f.y) * unit;
         }
+      }
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
         uint4 w[SETS];

@@ -18,9 +18,8 @@
 // one CTA takes the batches of one 64-byte column in order, elsewhere batches
 // are dealt out.
 // Measured: 16 sequences of up to 16000 slots cut to 2045, 8 x 128 bf16 into
-// other pages, 55 us: 18 us to select, bound by its passes' barriers, and 37 us
-// to move, 6.2 TB/s; one 12 x 64 fp32 sequence of 1024 slots cut to 512 8.7
-// us.
+// other pages, 52 us: 15 us to select, bound by its passes' barriers, and 37 us
+// to move, 6.2 TB/s; one 12 x 64 fp32 sequence of 1024 slots cut to 512, 8.5 us.
 #include <cooperative_groups.h>
 
 #include "kv_cache.cuh"

@@ -192,12 +192,22 @@ struct Layout {
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Brief: at most a tile of slots, whatever the batch (200 sequences of 16 slots,
-// 24 x 128 bf16 for 192 heads: 47 us against 56 us in matrices), or few slots
-// and few heads (4 sequences of 256 slots, 8 x 128 bf16 for 64 heads: 7.9 us
-// against 8.6 us; 16 of them: 14.7 us against 10.1 us).
+// Brief: slots too few for the matrix body, whose staging of the queries is then
+// most of its time. Plain lanes against matrices, 8 key-value heads:
+//   at most a tile of slots, whatever the batch: 200 sequences of 16 slots, 24 x
+//     128 bf16 for 192 heads, 47 us against 56 us;
+//   little work: 4 x 300 slots of 128 fp16 for 32 heads 7.5 us against 9.7 us, for
+//     64 heads 8.5 us against 10.2 us (4 x 1000 for 64: 15.3 us against 11.5 us);
+//     int8 for 32 heads 4 x 1000 10.0 us against 14.1 us (16 x 1000: 24 us
+//     against 22 us).
+// Rows of more than 128 elements of 16 bits are many registers to a plain lane
+// (4 x 300 of 192 bf16 for 32 heads: 10 us against 8.7 us), and int8 rows of up to 64
+// are as fast in matrices (1 x 1000 for 32 heads: 6.8 us against 5.4 us).
 AttendKernel choose(const w4kv::View& c, int type, int32_t group) {
-  const bool brief = c.capacity <= 16 || (c.capacity <= 256 && int64_t(c.seqs) * c.heads * group <= 256);
+  const bool i8 = type == W4_KV_I8;
+  const int64_t work = int64_t(c.seqs) * c.heads * ((group + 1) / 2) * c.capacity;
+  const bool brief = c.capacity <= 16 || (c.capacity <= 1024 && work <= (i8 && c.dim <= 128 ? 65536 : 40960) &&
+                                          (i8 ? c.dim > 64 : c.dim <= 128));
   switch (type) {
     case W4_KV_F32: return attend_kernel_for<W4_KV_F32>(c.dim, group, brief);
     case W4_KV_F16: return attend_kernel_for<W4_KV_F16>(c.dim, group, brief);
@@ -206,20 +216,23 @@ AttendKernel choose(const w4kv::View& c, int type, int32_t group) {
   }
 }
 
-// CTAs of a kernel that an SM holds (asked once for each kernel and device), in
-// runs of units and in warps' items.
-w4_status resident(const AttendKernel& k, int dev, int* out, int* warp_out) {
-  struct Known {
-    const void* fn;
-    int dev, n, warp_n;
-  };
-  static thread_local Known known[16] = {};
+constexpr int kRankLogs = 5;  // clusters of 1, 2, 4, 8 and 16 CTAs
+
+// What a device holds of a kernel at once, asked once for each kernel and device.
+struct Held {
+  const void* fn;
+  int dev;
+  int per_sm, warp_per_sm;    // CTAs an SM, in runs of units and in warps' items
+  int clusters[kRankLogs];    // clusters of 2^i CTAs: by GPC, so fewer than their CTAs alone
+};
+
+w4_status resident(const AttendKernel& k, const w4host::DeviceInfo& di, Held* out) {
+  static thread_local Held known[16] = {};
   static thread_local int next = 0;
   const void* fn = reinterpret_cast<const void*>(k.fn);
-  for (const Known& e : known)
-    if (e.fn == fn && e.dev == dev) {
-      *out = e.n;
-      *warp_out = e.warp_n;
+  for (const Held& e : known)
+    if (e.fn == fn && e.dev == di.dev) {
+      *out = e;
       return W4_OK;
     }
   const auto allow = [](void (*f)(const AttendParams), size_t smem) {
@@ -230,15 +243,36 @@ w4_status resident(const AttendKernel& k, int dev, int* out, int* warp_out) {
   if (e == cudaSuccess) e = allow(k.warp_fn, k.warp_smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k.item_fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return w4host::cuda_fail(e, "kv_attend kernel attributes");
-  int n = 0, warp_n = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k.fn, kAttendThreads, k.smem);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&warp_n, k.warp_fn, kAttendThreads, k.warp_smem);
+  Held h = {fn, di.dev, 0, 0, {}};
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h.per_sm, k.fn, kAttendThreads, k.smem);
+  if (e == cudaSuccess)
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h.warp_per_sm, k.warp_fn, kAttendThreads, k.warp_smem);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h.clusters[0], k.item_fn, kAttendThreads, k.smem);
   if (e != cudaSuccess) return w4host::cuda_fail(e, "kv_attend occupancy");
-  if (n < 1 || warp_n < 1) return w4host::fail(W4_ERR_CUDA, "kv_attend: no CTA fits an SM");
-  known[next] = {fn, dev, n, warp_n};
+  if (h.per_sm < 1 || h.warp_per_sm < 1 || h.clusters[0] < 1)
+    return w4host::fail(W4_ERR_CUDA, "kv_attend: no CTA fits an SM");
+  h.clusters[0] *= di.sms;
+  for (int i = 1; i < kRankLogs; ++i) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(1u << i);
+    cfg.blockDim = dim3(kAttendThreads);
+    cfg.dynamicSmemBytes = k.smem;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << i;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+    attr[1].val.sharedMemCarveout = cudaSharedmemCarveoutMaxShared;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaOccupancyMaxActiveClusters(&h.clusters[i], k.item_fn, &cfg) != cudaSuccess) {
+      cudaGetLastError();  // no such cluster on this device
+      h.clusters[i] = 0;
+    }
+  }
+  known[next] = h;
   next = (next + 1) % 16;
-  *out = n;
-  *warp_out = warp_n;
+  *out = h;
   return W4_OK;
 }
 
@@ -249,29 +283,31 @@ w4_status lay_out(const w4kv::View& c, int type, int64_t q_heads, bool with_acc,
   Layout L = {};
   L.kernel = choose(c, type, group);
   L.chunks = (group + L.kernel.rows - 1) / L.kernel.rows;
-  int per_sm = 0, warp_per_sm = 0;
-  const w4_status rc = resident(L.kernel, di.dev, &per_sm, &warp_per_sm);
+  Held held = {};
+  const w4_status rc = resident(L.kernel, di, &held);
   if (rc != W4_OK) return rc;
   const int64_t items = int64_t(c.seqs) * c.heads * L.chunks;
   const int64_t most = items * ((c.capacity + L.kernel.unit - 1) / L.kernel.unit + L.kernel.over);
   if (most > 0x7fffffff) return w4host::fail(W4_ERR_SHAPE, "seqs x heads x capacity are more slots than a call takes");
-  const int64_t wave = int64_t(per_sm) * sms;
+  const int64_t wave = int64_t(held.per_sm) * sms;
   // An item a cluster: the widest of up to 16 CTAs that one wave holds for all
   // items, where it leaves a CTA kMostUnits units of a full sequence. One
   // 12 x 64 fp32 sequence of 1021 slots: 5.5 us against 8.8 us as runs and a
   // join; 48 of 1024, bf16: 26 us against 33 us; 8 of 1000, 8 x 128 bf16 for 32
   // heads: 12.3 us against 16.1 us.
   const int64_t units = (c.capacity + L.kernel.unit - 1) / L.kernel.unit;
-  unsigned ranks = per_sm > 1 ? 16 : 8;  // wider than 8 is not given on every GPC where each CTA fills an SM
-  while (ranks > 1 && (items * ranks > wave || ranks / 2 >= units)) ranks /= 2;
-  L.ranks = items * ranks <= wave && units <= int64_t(kMostUnits) * ranks ? ranks : 0;
+  // (As many as the GPCs hold, not as their SMs' sum does: 32 clusters of 16 are
+  // one wave by the sum at 4 CTAs an SM, and took two.)
+  int log = kRankLogs - 1;
+  while (log > 0 && (items > held.clusters[log] || (1 << log) / 2 >= units)) --log;
+  L.ranks = items <= held.clusters[log] && units <= int64_t(kMostUnits) << log ? 1u << log : 0;
   // More items than a wave of CTAs, and all of them short. 400 sequences of 64
   // slots, 12 x 64 bf16: 17 us against 30 us in runs; 1000 of 100, fp16: 58 us
   // against 80 us; 200 of 200, 8 x 128 bf16 for 32 heads: 47 us against 46 us.
   L.warps = L.ranks == 0 && items > wave && c.capacity <= kShortUnits * L.kernel.unit;
   if (L.ranks != 0 || L.warps) {
-    const int64_t by_warp = std::min((items + kWarps - 1) / kWarps, int64_t(warp_per_sm) * sms);
-    L.ctas = static_cast<unsigned>(L.warps ? by_warp : items * ranks);
+    const int64_t by_warp = std::min((items + kWarps - 1) / kWarps, int64_t(held.warp_per_sm) * sms);
+    L.ctas = static_cast<unsigned>(L.warps ? by_warp : items * L.ranks);
     L.lse2 = 0;
     L.scores = with_acc ? round256(static_cast<size_t>(c.seqs) * q_heads * 4) : 0;
     L.bytes = L.scores + (with_acc ? static_cast<size_t>(c.seqs) * q_heads * c.capacity * 4 : 0);

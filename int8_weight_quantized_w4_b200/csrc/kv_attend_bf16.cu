@@ -5,7 +5,7 @@ namespace w4kv {
 
 template <>
 AttendKernel attend_kernel_for<W4_KV_BF16>(int32_t dim, int32_t group, bool brief) {
-  if (group >= 3 && !brief)
+  if (group >= least_group(dim) && !brief)
     return group <= 4 ? matrix_kernel_for<W4_KV_BF16, 4>(dim) : matrix_kernel_for<W4_KV_BF16, 8>(dim);
   return plain_kernel_for<W4_KV_BF16>(dim, group);
 }

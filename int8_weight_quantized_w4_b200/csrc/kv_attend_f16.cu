@@ -5,7 +5,7 @@ namespace w4kv {
 
 template <>
 AttendKernel attend_kernel_for<W4_KV_F16>(int32_t dim, int32_t group, bool brief) {
-  if (group >= 3 && !brief) return matrix_kernel_for<W4_KV_F16, 8>(dim);
+  if (group >= least_group(dim) && !brief) return matrix_kernel_for<W4_KV_F16, 8>(dim);
   return plain_kernel_for<W4_KV_F16>(dim, group);
 }
 

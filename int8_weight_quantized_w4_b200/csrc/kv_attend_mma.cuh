@@ -1,5 +1,5 @@
 // The matrix-instruction body of kv_attend, for several query heads on one
-// key-value head: at 4 heads and more the plain lanes' fused multiply-adds
+// key-value head: from 3 heads on the plain lanes' fused multiply-adds
 // (one for each head and stored element) take longer than the loads.
 //
 // Exactness. A stored key or value is an exact fp16 (fp16, int8 codes) or
@@ -379,6 +379,13 @@ struct MatrixLanes {
     return to;
   }
 };
+
+// Query heads of a key-value head from which on the matrices are faster, where
+// there are slots enough. Two heads, 16 sequences of 4000 slots of 8 key-value heads:
+// 64 bf16 30 us in plain lanes, 33 us in matrices; 128 int8 43 us, 49 us; 160
+// bf16 101 us, 62 us; 256 int8 111 us, 76 us. Three heads, 8 sequences of 6000
+// slots of 16 x 128 bf16: 124 us, 70 us.
+inline int32_t least_group(int32_t dim) { return dim > 128 ? 2 : 3; }
 
 // The matrix kernel for this many query heads, where there is one.
 template <int TYPE, int ROWS>

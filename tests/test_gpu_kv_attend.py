@@ -386,3 +386,19 @@ def test_attend_large_values(kind, group):
     # term at most 600 x 2^-24 off in its sum), the pieces' 2^-21 and, for int8, one rounding of the scale
     bound = 2 * n * 2.0 ** -24 + 2.0 ** -20
     assert float((out / 2.0 ** 96 - 1).abs().max()) <= bound
+
+
+@pytest.mark.parametrize("window", [0, 77])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("heads,group,dim,page", [
+    (2, 3, 48, 5), (1, 4, 128, 64), (2, 8, 64, 16), (1, 5, 80, 1), (1, 9, 256, 20), (1, 2, 160, 16), (2, 2, 256, 7),
+    (1, 16, 96, 3), (1, 7, 192, 16),
+])
+def test_attend_short_sequences_in_long_rooms(kind, heads, group, dim, page, window):
+    """Room for more slots than the plain lanes are taken for, few items: the
+    matrices (where there are heads enough), an item a cluster."""
+    rng = np.random.default_rng(heads * 1000 + group * 100 + dim + page + window)
+    lengths = [0, 1, 2, 15, 16, 17, 33, 64, 65, 130, 301, 1100]
+    cache, k, v = build(rng, kind, lengths, heads, dim, page, max_pages=room_for(1500, page))
+    q = rng.standard_normal((len(lengths), heads * group, dim)).astype(np.float32)
+    check(cache, k, v, q, window=window, with_acc=True, strided=True, what=f"{kind} {heads}x{group}x{dim}")

@@ -194,8 +194,9 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Brief: slots too few for the matrix body, whose staging of the queries is then
 // most of its time. Plain lanes against matrices, 8 key-value heads:
-//   at most a tile of slots, whatever the batch: 200 sequences of 16 slots, 24 x
-//     128 bf16 for 192 heads, 47 us against 56 us;
+//   a tile or two of slots, whatever the batch: 200 sequences of 32 slots of 256
+//     bf16 for 32 heads 32 us against 41 us, of 128 int8 16 us against 22 us (64
+//     slots: 26 us against 28 us; 32 of 64 bf16: 9.2 us against 6.7 us);
 //   little work: 4 x 300 slots of 128 fp16 for 32 heads 7.5 us against 9.7 us, for
 //     64 heads 8.5 us against 10.2 us (4 x 1000 for 64: 15.3 us against 11.5 us);
 //     int8 for 32 heads 4 x 1000 10.0 us against 14.1 us (16 x 1000: 24 us
@@ -203,10 +204,11 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 // Rows of more than 128 elements of 16 bits are many registers to a plain lane
 // (4 x 300 of 192 bf16 for 32 heads: 10 us against 8.7 us), and int8 rows of up to 64
 // are as fast in matrices (1 x 1000 for 32 heads: 6.8 us against 5.4 us).
-AttendKernel choose(const w4kv::View& c, int type, int32_t group) {
+// slots: the most that a sequence attends.
+AttendKernel choose(const w4kv::View& c, int type, int32_t group, int64_t slots) {
   const bool i8 = type == W4_KV_I8;
-  const int64_t work = int64_t(c.seqs) * c.heads * ((group + 1) / 2) * c.capacity;
-  const bool brief = c.capacity <= 16 || (c.capacity <= 1024 && work <= (i8 && c.dim <= 128 ? 65536 : 40960) &&
+  const int64_t work = int64_t(c.seqs) * c.heads * ((group + 1) / 2) * slots;
+  const bool brief = slots <= (c.dim < 128 ? 16 : 32) || (slots <= 1024 && work <= (i8 && c.dim <= 128 ? 65536 : 40960) &&
                                           (i8 ? c.dim > 64 : c.dim <= 128));
   switch (type) {
     case W4_KV_F32: return attend_kernel_for<W4_KV_F32>(c.dim, group, brief);
@@ -276,18 +278,21 @@ w4_status resident(const AttendKernel& k, const w4host::DeviceInfo& di, Held* ou
   return W4_OK;
 }
 
-w4_status lay_out(const w4kv::View& c, int type, int64_t q_heads, bool with_acc, const w4host::DeviceInfo& di,
-                  Layout* out) {
+// kernel: as chosen for `slots` or more. For one kernel, fewer slots never need
+// more workspace.
+w4_status lay_out(const w4kv::View& c, const AttendKernel& kernel, int64_t slots, int64_t q_heads, bool with_acc,
+                  const w4host::DeviceInfo& di, Layout* out) {
   const int sms = di.sms;
   const int32_t group = static_cast<int32_t>(q_heads / c.heads);
   Layout L = {};
-  L.kernel = choose(c, type, group);
+  L.kernel = kernel;
   L.chunks = (group + L.kernel.rows - 1) / L.kernel.rows;
   Held held = {};
   const w4_status rc = resident(L.kernel, di, &held);
   if (rc != W4_OK) return rc;
   const int64_t items = int64_t(c.seqs) * c.heads * L.chunks;
-  const int64_t most = items * ((c.capacity + L.kernel.unit - 1) / L.kernel.unit + L.kernel.over);
+  const int64_t units = (slots + L.kernel.unit - 1) / L.kernel.unit;
+  const int64_t most = items * (units + L.kernel.over);
   if (most > 0x7fffffff) return w4host::fail(W4_ERR_SHAPE, "seqs x heads x capacity are more slots than a call takes");
   const int64_t wave = int64_t(held.per_sm) * sms;
   // An item a cluster: the widest of up to 16 CTAs that one wave holds for all
@@ -295,7 +300,6 @@ w4_status lay_out(const w4kv::View& c, int type, int64_t q_heads, bool with_acc,
   // 12 x 64 fp32 sequence of 1021 slots: 5.5 us against 8.8 us as runs and a
   // join; 48 of 1024, bf16: 26 us against 33 us; 8 of 1000, 8 x 128 bf16 for 32
   // heads: 12.3 us against 16.1 us.
-  const int64_t units = (c.capacity + L.kernel.unit - 1) / L.kernel.unit;
   // (As many as the GPCs hold, not as their SMs' sum does: 32 clusters of 16 are
   // one wave by the sum at 4 CTAs an SM, and took two.)
   int log = kRankLogs - 1;
@@ -304,7 +308,7 @@ w4_status lay_out(const w4kv::View& c, int type, int64_t q_heads, bool with_acc,
   // More items than a wave of CTAs, and all of them short. 400 sequences of 64
   // slots, 12 x 64 bf16: 17 us against 30 us in runs; 1000 of 100, fp16: 58 us
   // against 80 us; 200 of 200, 8 x 128 bf16 for 32 heads: 47 us against 46 us.
-  L.warps = L.ranks == 0 && items > wave && c.capacity <= kShortUnits * L.kernel.unit;
+  L.warps = L.ranks == 0 && items > wave && slots <= kShortUnits * L.kernel.unit;
   if (L.ranks != 0 || L.warps) {
     const int64_t by_warp = std::min((items + kWarps - 1) / kWarps, int64_t(held.warp_per_sm) * sms);
     L.ctas = static_cast<unsigned>(L.warps ? by_warp : items * L.ranks);
@@ -336,11 +340,18 @@ extern "C" size_t kv_attend_workspace_size(const kv_cache* c, int64_t q_heads, i
   using namespace w4host;
   w4kv::View v;
   const DeviceInfo* di = nullptr;
-  Layout L;
   if (check_cache(c, "cache", &v) != W4_OK || check_heads(v, q_heads) != W4_OK || c->seqs == 0 ||
-      current_device(&di) != W4_OK || lay_out(v, c->type, q_heads, with_acc != 0, *di, &L) != W4_OK)
+      current_device(&di) != W4_OK)
     return 0;
-  return L.bytes;
+  // a window may choose another kernel: the larger need of both
+  const int32_t group = static_cast<int32_t>(q_heads / v.heads);
+  size_t bytes = 0;
+  for (const int64_t slots : {int64_t(v.capacity), int64_t(1)}) {
+    Layout L;
+    if (lay_out(v, choose(v, c->type, group, slots), v.capacity, q_heads, with_acc != 0, *di, &L) != W4_OK) return 0;
+    bytes = std::max(bytes, L.bytes);
+  }
+  return bytes;
 }
 
 extern "C" w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, int64_t q_heads, float scale,
@@ -368,7 +379,9 @@ extern "C" w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, i
   rc = current_device(&di);
   if (rc != W4_OK) return rc;
   Layout L;
-  rc = lay_out(p.c, c->type, q_heads, acc != nullptr, *di, &L);
+  const int64_t slots = window > 0 ? std::min(window, int64_t(p.c.capacity)) : p.c.capacity;
+  const AttendKernel kernel = choose(p.c, c->type, static_cast<int32_t>(q_heads / c->kv_heads), slots);
+  rc = lay_out(p.c, kernel, slots, q_heads, acc != nullptr, *di, &L);
   if (rc != W4_OK) return rc;
   if (L.bytes > 0 && (workspace == nullptr || workspace_bytes < L.bytes))
     return fail(W4_ERR_WORKSPACE, "kv_attend needs a workspace of %zu bytes, %zu given", L.bytes,

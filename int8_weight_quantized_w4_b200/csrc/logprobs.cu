@@ -268,13 +268,19 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
       // NaN is never the maximum, and only matters where fewer than `top` others are there
       if (__any_sync(0xffffffffu, !(top < bar_x))) {
         raise(*static_cast<volatile Key*>(&cta_bar));
+        // those that may be wanted, a bit each; a warp takes one of each lane at a time
+        uint32_t hits = 0;
 #pragma unroll
-        for (int u = 0; u < kQuads; ++u) {
-          const int32_t at = q + u * kThreads + lane;
-          const bool there = at < q1;
-          const int32_t id = lead + 4 * at;
+        for (int i = 0; i < 4 * kQuads; ++i)
+          hits |= static_cast<uint32_t>(q + i / 4 * kThreads + lane < q1 && !(w[i] < bar_x)) << i;
+        while (__any_sync(0xffffffffu, hits != 0)) {
+          const int i = hits != 0 ? __ffs(hits) - 1 : 0;
+          float x = w[0];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) offer(w[4 * u + e], id + e, there);
+          for (int j = 1; j < 4 * kQuads; ++j) x = i == j ? w[j] : x;
+          const Key k = logit_key(x, static_cast<uint32_t>(lead + 4 * (q + i / 4 * kThreads + lane) + i % 4));
+          insert(list, k, hits != 0 && k >= bar, lane);
+          hits &= hits - 1;
         }
         const Key last = shfl_key(list, p.top - 1);
         if (last > bar) {

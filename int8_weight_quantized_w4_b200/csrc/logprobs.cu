@@ -272,13 +272,16 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
         uint32_t hits = 0;
 #pragma unroll
         for (int i = 0; i < 4 * kQuads; ++i)
-          hits |= static_cast<uint32_t>(q + i / 4 * kThreads + lane < q1 && !(w[i] < bar_x)) << i;
+          hits |= static_cast<uint32_t>(!(w[i] < bar_x)) << i;
+        if (bar_x == -INFINITY) {  // which is also what is not there
+#pragma unroll
+          for (int u = 0; u < kQuads; ++u)
+            if (q + u * kThreads + lane >= q1) hits &= ~(15u << (4 * u));
+        }
         while (__any_sync(0xffffffffu, hits != 0)) {
           const int i = hits != 0 ? __ffs(hits) - 1 : 0;
-          float x = w[0];
-#pragma unroll
-          for (int j = 1; j < 4 * kQuads; ++j) x = i == j ? w[j] : x;
-          const Key k = logit_key(x, static_cast<uint32_t>(lead + 4 * (q + i / 4 * kThreads + lane) + i % 4));
+          const int32_t id = lead + 4 * (q + i / 4 * kThreads + lane) + i % 4;
+          const Key k = hits != 0 ? logit_key(__ldg(x + id), static_cast<uint32_t>(id)) : 0;  // near: it was just read
           insert(list, k, hits != 0 && k >= bar, lane);
           hits &= hits - 1;
         }

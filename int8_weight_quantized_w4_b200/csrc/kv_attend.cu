@@ -229,7 +229,7 @@ struct Held {
 };
 
 w4_status resident(const AttendKernel& k, const w4host::DeviceInfo& di, Held* out) {
-  static thread_local Held known[16] = {};
+  static thread_local Held known[32] = {};
   static thread_local int next = 0;
   const void* fn = reinterpret_cast<const void*>(k.fn);
   for (const Held& e : known)
@@ -273,7 +273,7 @@ w4_status resident(const AttendKernel& k, const w4host::DeviceInfo& di, Held* ou
     }
   }
   known[next] = h;
-  next = (next + 1) % 16;
+  next = (next + 1) % 32;
   *out = h;
   return W4_OK;
 }

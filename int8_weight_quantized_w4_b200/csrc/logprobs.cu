@@ -15,8 +15,9 @@
 // one of any warp of the CTA (of n unordered logits about top * ln(n / top)
 // pass); to begin with, the top-th largest of the threads' first maxima is such
 // a bound. Lists and sums are joined pairwise by as many warps. Bound by
-// reading the logits (2048 rows of 50257: 69.5 us, 5.9 TB/s), by latency where
-// there are few (one row with 5 alternatives: 7.5 us; 58 rows with 20: 11.8 us).
+// reading the logits (2048 rows of 50257: 69 us, 6.0 TB/s; with 20 alternatives
+// by the insertions, 94 us), by latency where there are few (one row with 5
+// alternatives: 6.9 us; 58 rows with 20: 11.4 us).
 #include <cooperative_groups.h>
 
 #include "kv_cache.cuh"
@@ -365,7 +366,8 @@ extern "C" w4_status token_logprobs(const float* logits, int64_t ldl, const int3
   if (rc != W4_OK) return rc;
   const LogprobParams p = {logits, ldl, tokens, static_cast<int32_t>(V), top, logp, entropy, top_logp, top_ids, di->err};
   // CTAs of a row: up to 8, while the rows alone do not give every SM four and
-  // a CTA has a few thousand logits or more
+  // a CTA has a few thousand logits or more. 134 rows of 95490: 1 CTA 19.2 us, 2
+  // 15.4, 4 (this rule's) 12.0, 8 15.6; 618 of 45918: 1 (this rule's) 27 us, 2 29 us
   unsigned ranks = 1;
   while (ranks < 8 && M * ranks * 2 <= 4 * di->sms && V / (ranks * 2) >= 8 * kThreads) ranks *= 2;
   const cudaError_t e = launch_pdl(top > 0 ? logprob_kernel<true> : logprob_kernel<false>,

@@ -402,3 +402,38 @@ def test_attend_short_sequences_in_long_rooms(kind, heads, group, dim, page, win
     cache, k, v = build(rng, kind, lengths, heads, dim, page, max_pages=room_for(1500, page))
     q = rng.standard_normal((len(lengths), heads * group, dim)).astype(np.float32)
     check(cache, k, v, q, window=window, with_acc=True, strided=True, what=f"{kind} {heads}x{group}x{dim}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [7, 160])
+@pytest.mark.parametrize("window", [1, 20, 200, 1300])
+def test_attend_window_decides_the_body(kind, n, window):
+    """A window far below the room: another body and launch than without one,
+    in the workspace that fits every window."""
+    rng = np.random.default_rng(n + window)
+    lengths = [int(x) for x in rng.integers(0, 1500, n)]
+    lengths[0], lengths[-1] = 0, 1400
+    cache, k, v = build(rng, kind, lengths, 2, 32, 16, max_pages=room_for(20000, 16))
+    q = rng.standard_normal((n, 8, 32)).astype(np.float32)
+    check(cache, k, v, q, window=window, with_acc=n < 10, what=f"window {window} of {n}")
+
+
+def test_attend_most_sequences():
+    """65535 of them, over one row of pages."""
+    T = torch()
+    B, cap, dim = 65535, 40, 16
+    rng = np.random.default_rng(91)
+    rows = rng.standard_normal((2, cap // 8, 1, 8, dim)).astype(np.float32)
+    k, v = (T.from_numpy(x).cuda() for x in rows)
+    table = T.arange(cap // 8, dtype=T.int32, device="cuda").view(1, -1).expand(B, -1)
+    lengths = (T.arange(B, device="cuda") % (cap + 1)).to(T.int32)
+    cache = w4().KvCache(k, v, table, lengths)
+    q = T.from_numpy(rng.standard_normal((B, 2, dim)).astype(np.float32)).cuda()
+    clear_error()
+    out = w4().kv_attend(q, cache)
+    assert error_status() == 0
+    flat = rows.astype(np.float64).reshape(2, cap, 1, dim)
+    for b in [*range(0, B, 1009), B - 1]:
+        n = int(lengths[b])
+        ro, _, _, (to, _, _) = oracle.kv_attend_ref(q[b].cpu().numpy(), flat[0, :n], flat[1, :n], dim ** -0.5)
+        assert np.all(np.abs(out[b].cpu().double().numpy() - ro) <= to), b

@@ -129,6 +129,7 @@ __device__ __forceinline__ void log_sums(const AttendParams& p, int32_t b, int32
 // and every 8th head; the warps' sums are added in their order.
 __device__ __forceinline__ void gather_weights(const AttendParams& p, int block, int blocks, int32_t b, float* acc,
                                                int64_t ldacc, bool runs) {
+  constexpr int kAhead = 4;
   __shared__ float sums[kJoinWarps][32];
   __shared__ float z[kJoinThreads];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -138,17 +139,29 @@ __device__ __forceinline__ void gather_weights(const AttendParams& p, int block,
   for (int64_t j0 = lo + int64_t(block) * 32; j0 < n; j0 += int64_t(blocks) * 32) {
     const int64_t j = j0 + lane;
     float sum = 0.f;
+    const float old = warp == 0 && j < n ? acc[int64_t(b) * ldacc + j] : 0.f;
     for (int q0 = 0; q0 < q_heads; q0 += kJoinThreads) {
       const int heads = min(kJoinThreads, q_heads - q0);
+      const float* x = p.scores + (int64_t(b) * q_heads + q0) * p.c.capacity + j;
+      float ahead[kAhead];  // on their way while the log sums are made
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = warp + u * kJoinWarps;
+        ahead[u] = j < n && i < heads ? x[int64_t(i) * p.c.capacity] : 0.f;
+      }
       if (q_heads > kJoinThreads || j0 == lo + int64_t(block) * 32) {
         __syncthreads();
         log_sums(p, b, q0, heads, runs, z);
         __syncthreads();
       }
-      const float* x = p.scores + (int64_t(b) * q_heads + q0) * p.c.capacity + j;
       if (j < n) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int i = warp + u * kJoinWarps;
+          if (i < heads) sum += z[i] == -INFINITY ? 0.f : ex2(ahead[u] - z[i]);
+        }
 #pragma unroll 4
-        for (int i = warp; i < heads; i += kJoinWarps)
+        for (int i = warp + kAhead * kJoinWarps; i < heads; i += kJoinWarps)
           sum += z[i] == -INFINITY ? 0.f : ex2(x[int64_t(i) * p.c.capacity] - z[i]);
       }
     }
@@ -157,7 +170,7 @@ __device__ __forceinline__ void gather_weights(const AttendParams& p, int block,
     if (warp == 0 && j < n) {
 #pragma unroll
       for (int w = 1; w < kJoinWarps; ++w) sum += sums[w][lane];
-      acc[int64_t(b) * ldacc + j] += sum;
+      acc[int64_t(b) * ldacc + j] = old + sum;
     }
     __syncthreads();
   }

@@ -309,15 +309,18 @@ w4_status lay_out(const w4kv::View& c, const AttendKernel& kernel, int64_t slots
   if (most > 0x7fffffff) return w4host::fail(W4_ERR_SHAPE, "seqs x heads x capacity are more slots than a call takes");
   const int64_t wave = int64_t(held.per_sm) * sms;
   // An item a cluster: the widest of up to 16 CTAs that one wave holds for all
-  // items, where it leaves a CTA kMostUnits units of a full sequence. One
+  // items, where it leaves a CTA kMostUnits units (of 64 slots at most) of a full
+  // sequence: runs balance the CTAs, clusters save the second launch. One
   // 12 x 64 fp32 sequence of 1021 slots: 5.5 us against 8.8 us as runs and a
   // join; 48 of 1024, bf16: 26 us against 33 us; 8 of 1000, 8 x 128 bf16 for 32
-  // heads: 12.3 us against 16.1 us.
+  // heads: 12.3 us against 16.1 us; twice the units, 48 of up to 2048, 33.5 us
+  // against 32.3 us; 32 of up to 2000, 8 x 128 int8 for 64 heads, 41 us against 37 us.
   // (As many as the GPCs hold, not as their SMs' sum does: 32 clusters of 16 are
   // one wave by the sum at 4 CTAs an SM, and took two.)
   int log = kRankLogs - 1;
   while (log > 0 && (items > held.clusters[log] || (1 << log) / 2 >= units)) --log;
-  L.ranks = items <= held.clusters[log] && units <= int64_t(kMostUnits) << log ? 1u << log : 0;
+  const int64_t most_slots = int64_t(kMostUnits) * std::min(64, L.kernel.unit) << log;
+  L.ranks = items <= held.clusters[log] && slots <= most_slots ? 1u << log : 0;
   // More items than a wave of CTAs, and all of them short. 400 sequences of 64
   // slots, 12 x 64 bf16: 17 us against 30 us in runs; 1000 of 100, fp16: 58 us
   // against 80 us; 200 of 200, 8 x 128 bf16 for 32 heads: 47 us against 46 us.

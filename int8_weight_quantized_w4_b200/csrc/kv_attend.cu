@@ -65,7 +65,7 @@ __device__ __forceinline__ void join_heads(const AttendParams& p, int wpr) {
     attended(p, b, lo, n);
     const int2 meta = n > lo ? meta_of(p, b, qh, &g) : make_int2(0, 0);
     work = meta.y != 1;
-#pragma unroll 2
+#pragma unroll 8
     for (int32_t i = sub; i < (work ? meta.y : 0); i += wpr) {
       const float* part = partial(p, meta, i);
 #pragma unroll

@@ -623,8 +623,8 @@ W4_API w4_status kv_append(const kv_cache* c, const float* k, int64_t ldk, const
  * Sums and the softmax are fp32; K and V enter with their stored values. A
  * NaN or Inf in q or in an attended slot makes the rows that it reaches
  * non-finite; what lies in other slots has no effect. The weighted values are
- * summed before they are divided, with weights of up to 2^7 (fp16 and int8:
- * 2^14): stored values beyond 2^96 may overflow there. Results do not depend
+ * summed before they are divided, with weights of up to 2^7 (fp16: 2^14):
+ * stored values beyond 2^96 may overflow there. Results do not depend
  * on timing: the same call gives the same bits. */
 W4_API size_t kv_attend_workspace_size(const kv_cache* c, int64_t q_heads, int32_t with_acc);
 W4_API w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, int64_t q_heads, float scale,

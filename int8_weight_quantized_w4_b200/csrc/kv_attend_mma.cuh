@@ -10,7 +10,13 @@
 //               exact rest, scaled by 2^11. Queries are scaled by a power of
 //               two so that their largest lies at 2^14, weights so that it lies
 //               from 2^7 to 2^14: what is left out is below 2^-22 of each of
-//               them or 2^-43 of the largest;
+//               them or 2^-43 of the largest. int8's weights have the value's
+//               scale in them, and the largest of those products counts, each
+//               head's own and from 2^8 on (2^-44): a slot whose scale is
+//               large but whose weight is not takes no bits from the others.
+//               Nor does a row of zeros, whatever its scale (kv_append gives
+//               it 1): where a product would raise the power, such rows'
+//               are set to 0 first;
 //   bf16:       4 heads x 3 pieces (8 + 8 + 8 bits, all of them) in one
 //               instruction, or 8 heads in two (pieces 0 and 1, then 2).
 //
@@ -108,7 +114,10 @@ struct MatrixLanes {
   static constexpr int NT = I8 && MAXD <= 128 ? 2 : 1;  // 16 slots each, at once: int8's stages have room for two
   static constexpr int TS = 16 * NT;
   static constexpr int kLift = 14;  // fp16 pieces: the exponent of the largest query, and of the largest weight
-  static constexpr float kBelow = BF ? 0.f : kLift - kSlack;  // a new reference lies this far below the maximum
+  static constexpr float kBelow = BF || I8 ? 0.f : kLift - kSlack;  // a new reference lies this far below the maximum
+  static constexpr int kFresh = 8;  // int8: a new power lifts the largest product of weight and scale to here,
+                                    // and stands until one passes 2^(kLift + 1)
+  static constexpr int kMostUp = 126;  // the largest power
   static constexpr int kFrag = SETS * STEPS * 32 * 4;   // words of the queries' operands
   static constexpr int kWidth = MAXD;  // of a row of queries in shared memory
   static constexpr int kBodyFloats = kFrag;
@@ -184,6 +193,18 @@ struct MatrixLanes {
     return v;
   }
 
+  // 2^by, by <= 0; below fp32's normal numbers nothing is left but a NaN.
+  __device__ static __forceinline__ float falling(int by) { return by < -126 ? 0.f : power_of_two(by); }
+
+  // The largest of this lane's weights in a tile.
+  __device__ static __forceinline__ float largest(const float (&x)[2 * NT][2]) {
+    float top = 0.f;
+#pragma unroll
+    for (int n = 0; n < 2 * NT; ++n) top = fmaxf(top, fmaxf(fabsf(x[n][0]), fabsf(x[n][1])));
+    return top;
+  }
+  __device__ static __forceinline__ int exponent(float x) { return static_cast<int>(__float_as_uint(x) >> 23) - 127; }
+
   // The warp's triple of its share (one of TEAM) of the segment: where it has been put.
   template <int TEAM>
   __device__ static __forceinline__ float* segment(const AttendParams& p, const Run& run, const Segment& seg, Feed& feed,
@@ -197,7 +218,7 @@ struct MatrixLanes {
     float acc[NC * VE][4];
 #pragma unroll
     for (int i = 0; i < NC * VE; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    int vexp = 1;  // int8: exponent field of the largest value scale so far; acc is in units of 2^(vexp - 127)
+    int up = kMostUp;  // int8: the weights' products with the values' scales enter times 2^up, which acc is in
 #pragma unroll 1
     for (int32_t tile = seg.s0 + warp * TS; tile < s1; tile += TEAM * TS) {
       uint32_t held;
@@ -271,30 +292,20 @@ struct MatrixLanes {
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // weights are 2^(x - m): m follows the maximum when that passes it by more
       // than what keeps the largest weight below 2^kLift
-      float back = 1.f;
+      float back = 1.f;  // what acc is multiplied by
       if (top - kBelow > m + kSlack) {
         top -= kBelow;
-        if (m != -INFINITY) back = ex2(m - top);  // without a score so far there are zeros, or a NaN
-        l *= back;
-        m = top;
-      }
-      float unit = 1.f;
-      if constexpr (I8) {
-        const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(scales[TS + lane % TS]))) >> 23);
-        const int now = max(vexp, min(e, 253));
-        const int fall = vexp - now;
-        if (fall != 0) back = fall < -126 ? back * 0.f : back * power_of_two(fall);
-        vexp = now;
-        unit = power_of_two(127 - now);
-      }
-      if (__any_sync(0xffffffffu, back != 1.f)) {
-#pragma unroll
-        for (int i = 0; i < NC * VE; ++i) {
-          acc[i][0] *= back;
-          acc[i][1] *= back;
-          acc[i][2] *= back;
-          acc[i][3] *= back;
+        if constexpr (I8) top = ceilf(top);  // references whole powers apart: acc keeps its own
+        const float fall = m == -INFINITY ? 1.f : ex2(m - top);  // without a score so far there are zeros, or a NaN
+        l *= fall;
+        if constexpr (I8) {
+          const int to = up + static_cast<int>(fminf(top - m, 1000.f));
+          up = min(to, kMostUp);
+          back = falling(up - to);
+        } else {
+          back = fall;
         }
+        m = top;
       }
       const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
@@ -305,7 +316,50 @@ struct MatrixLanes {
         for (int e = 0; e < 2; ++e) {
           x[n][e] = ex2(x[n][e] - ref);
           l += x[n][e];
-          if constexpr (I8) x[n][e] *= (e == 0 ? f.x : f.y) * unit;
+          if constexpr (I8) x[n][e] *= e == 0 ? f.x : f.y;
+        }
+      }
+      bool rescale = back != 1.f;
+      if constexpr (I8) rescale = rescale || exponent(largest(x)) + up > kLift;
+      if (__any_sync(0xffffffffu, rescale)) {
+        if constexpr (I8) {
+          uint32_t codes = 0;  // which of this lane's slots hold other codes than 0
+#pragma unroll
+          for (int n = 0; n < 4 * NT; ++n)
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+              for (int i = 0; i < VB / 4; ++i)
+                if ((g + 8 * cc) * VB < D && word(vx[n][cc], i) != 0u) codes |= 1u << n;
+#pragma unroll
+          for (int o = 4; o < 32; o *= 2) codes |= __shfl_xor_sync(0xffffffffu, codes, o);
+#pragma unroll
+          for (int n = 0; n < 2 * NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!((codes >> (2 * n + e)) & 1u)) x[n][e] *= 0.f;  // a scale of NaN stays
+          float most = largest(x);  // of the head's four lanes
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+          if (exponent(most) + up > kLift) {
+            back *= falling(kFresh - exponent(most) - up);
+            up = kFresh - exponent(most);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < NC * VE; ++i) {
+          acc[i][0] *= back;
+          acc[i][1] *= back;
+          acc[i][2] *= back;
+          acc[i][3] *= back;
+        }
+      }
+      if constexpr (I8) {
+        const float unit = power_of_two(up);
+#pragma unroll
+        for (int n = 0; n < 2 * NT; ++n) {
+          x[n][0] *= unit;
+          x[n][1] *= unit;
         }
       }
 #pragma unroll
@@ -362,7 +416,7 @@ struct MatrixLanes {
     }
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
-    const float unit = I8 ? power_of_two(vexp - 127) : 1.f;
+    const float unit = I8 ? power_of_two(-up) : 1.f;
     float* to = feed.spare();
     if (t == 0 && g < ROWS) {
       to[ROWS * D + head] = m;

@@ -437,3 +437,50 @@ def test_attend_most_sequences():
         n = int(lengths[b])
         ro, _, _, (to, _, _) = oracle.kv_attend_ref(q[b].cpu().numpy(), flat[0, :n], flat[1, :n], dim ** -0.5)
         assert np.all(np.abs(out[b].cpu().double().numpy() - ro) <= to), b
+
+
+@pytest.mark.parametrize("room", ROOMS)
+@pytest.mark.parametrize("group,dim", [(1, 64), (4, 64), (8, 128), (5, 192), (8, 256)])
+@pytest.mark.parametrize("where", ["zeros", "zeros first", "negligible", "outweighed"])
+def test_attend_int8_scales_of_slots_that_add_nothing(where, group, dim, room):
+    """Values of 1e-8 to 1e-11 beside slots whose large scale adds nothing:
+    rows of zeros (stored with scale 1), one slot of negligible weight, and one
+    that weighed everything until later slots outweighed it.
+
+    Bound: the definition's (score errors, roundings of the sums) relative to
+    sum w |v|; and what the weights' two fp16 pieces leave out, 2^-36 for each
+    code (127 at most) while the largest product of a weight and a scale, rows
+    of zeros aside, lies at 2^8 or above: 127 n 2^-44 of that product."""
+    T = torch()
+    rng = np.random.default_rng(group * dim)
+    n, heads = 700, 2
+    cache, _, _ = build(rng, "int8", [n], heads, dim, 16, max_pages=room_for(room, 16))
+    k = rng.standard_normal((n, heads, dim)).astype(np.float32)
+    v = (rng.standard_normal((n, heads, dim)) * 10.0 ** -rng.uniform(8, 11)).astype(np.float32)
+    k[:, :, 0] = 0.0  # the queries' first element is such that this one is added to the score
+    if where == "zeros":
+        v[rng.integers(0, n, 60)] = 0.0
+    elif where == "zeros first":
+        v[:65] = 0.0
+    elif where == "negligible":
+        k[5, :, 0], v[5] = -40.0, v[5] * 1e13
+    else:
+        k[:n // 2, :, 0], v[5] = -40.0, v[5] * 1e10
+    q = rng.standard_normal((1, heads * group, dim)).astype(np.float32)
+    q[:, :, 0] = dim ** 0.5
+    j = np.arange(n)
+    page = T.from_numpy(cache.page_table[0].cpu().numpy()[j // 16].astype(np.int64)).cuda()
+    inner = T.from_numpy(j % 16).cuda()
+    rows = []
+    for x, codes, scales in ((k, cache.k, cache.k_scales), (v, cache.v, cache.v_scales)):
+        c, s = oracle.kv_store(x, "int8")
+        codes[page, :, inner], scales[page, :, inner] = T.from_numpy(c).cuda(), T.from_numpy(s).cuda()
+        rows.append((oracle.kv_values(c, s), np.where(c.any(-1), s, 0.0)))
+    (k, _), (v, s) = rows
+    out = w4().kv_attend(T.from_numpy(q).cuda(), cache).cpu().double().numpy()[0]
+    ro, _, w, (_, _, tw) = oracle.kv_attend_ref(q[0], k, v, dim ** -0.5)
+    for i in range(heads * group):
+        h = i // group
+        bound = tw[i] @ np.abs(v[:, h]) + 127 * n * 2.0 ** -44 * (w[i] * s[:, h]).max()
+        off = np.abs(out[i] - ro[i])
+        assert np.all(off <= bound), f"head {i}: off by {np.max(off / bound):.3g} bounds, {np.max(off) / np.abs(ro[i]).max():.3g} of the result"

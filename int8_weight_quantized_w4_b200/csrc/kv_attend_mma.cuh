@@ -22,7 +22,8 @@
 //
 // Layout. mma.m16n8k16 sums over k in any order, and its n columns may be any
 // 8 values, so both operands are read from the stages as they were stored, 16
-// bytes a lane, without a transposing load: lane (g, t) = (lane / 4, lane % 4) reads
+// bytes a lane (values: VB), without a transposing load: lane (g, t) =
+// (lane / 4, lane % 4) reads
 //   keys:   vectors t, t + 4, ... of slots g and g + 8 of a tile's 16; the 8
 //           elements of a vector are two k-steps' 4 each;
 //   values: vectors g, g + 8 of slots 2t, 2t+1, 2t+8, 2t+9; byte permutes pair
@@ -108,7 +109,10 @@ struct MatrixLanes {
   static constexpr int EPV = E::kPerVec;
   static constexpr int NI = (MAXD / EPV + 3) / 4;       // key vectors of a lane
   static constexpr int STEPS = NI * EPV / 4;            // k-steps of the scores
-  static constexpr int VB = I8 && MAXD <= 64 ? 8 : 16;  // bytes of a value load
+  // bytes of a value load: shorter ones need fewer registers at a time. 32
+  // sequences of up to 6000 slots of 128 int8: 60.5 us with 16 bytes, 53.7 us with
+  // 8; fp16 57.9 us, 54.2 us; bf16 of 256 for 2 heads 24.6 us, 25.8 us
+  static constexpr int VB = BF && MAXD == 256 ? 16 : 8;
   static constexpr int VE = VB / E::kBytes;             // its elements
   static constexpr int NC = (MAXD / VE + 7) / 8;        // value vectors of a lane
   static constexpr int NT = I8 && MAXD <= 128 ? 2 : 1;  // 16 slots each, at once: int8's stages have room for two
@@ -186,11 +190,32 @@ struct MatrixLanes {
 
   // Rows of one head's pieces summed: in a lane, and over the two lanes that
   // share a head where there are 4.
-  __device__ static __forceinline__ float joined(float lo, float hi) {
-    if constexpr (!BF) return fmaf(hi, 1.f / 2048.f, lo);
-    float v = lo + hi;
+  __device__ static __forceinline__ float in_lane(float lo, float hi) { return BF ? lo + hi : fmaf(hi, 1.f / 2048.f, lo); }
+  __device__ static __forceinline__ float over_lanes(float v) {
     if constexpr (ROWS == 4) v += __shfl_xor_sync(0xffffffffu, v, 16);
     return v;
+  }
+  __device__ static __forceinline__ float joined(float lo, float hi) { return over_lanes(in_lane(lo, hi)); }
+  // A product's two columns to acc, as packed pairs; bf16's 8 rows have no
+  // registers for their alignment (16 x 4096 slots of 128 for 64 heads: 62 us
+  // packed, 58 us so; fp16: 54 us).
+  __device__ static __forceinline__ void add(float (&acc)[2], const float (&c)[4]) {
+    if constexpr (BF && ROWS == 8) {
+      acc[0] += in_lane(c[0], c[2]);
+      acc[1] += in_lane(c[1], c[3]);
+      return;
+    }
+    unsigned long long a, lo, hi;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(acc[0]), "f"(acc[1]));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(lo) : "f"(c[0]), "f"(c[1]));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(hi) : "f"(c[2]), "f"(c[3]));
+    if constexpr (BF) {
+      asm("add.rn.f32x2 %0, %0, %1;" : "+l"(lo) : "l"(hi));
+    } else {
+      asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(lo) : "l"(hi), "l"(0x3A0000003A000000ull));  // 2^-11 twice
+    }
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(lo));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[0]), "=f"(acc[1]) : "l"(a));
   }
 
   // 2^by, by <= 0; below fp32's normal numbers nothing is left but a NaN.
@@ -215,9 +240,9 @@ struct MatrixLanes {
     const int32_t s1 = seg.s1;
     const float scale = stage_queries<TEAM>(frag, sq) * p.scale2;
     float m = -INFINITY, l = 0.f;
-    float acc[NC * VE][4];
+    float acc[NC * VE][2];  // the lane's pieces added up
 #pragma unroll
-    for (int i = 0; i < NC * VE; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    for (int i = 0; i < NC * VE; ++i) acc[i][0] = acc[i][1] = 0.f;
     int up = kMostUp;  // int8: the weights' products with the values' scales enter times 2^up, which acc is in
 #pragma unroll 1
     for (int32_t tile = seg.s0 + warp * TS; tile < s1; tile += TEAM * TS) {
@@ -350,8 +375,6 @@ struct MatrixLanes {
         for (int i = 0; i < NC * VE; ++i) {
           acc[i][0] *= back;
           acc[i][1] *= back;
-          acc[i][2] *= back;
-          acc[i][3] *= back;
         }
       }
       if constexpr (I8) {
@@ -362,14 +385,14 @@ struct MatrixLanes {
           x[n][1] *= unit;
         }
       }
+      uint4 w[NT][SETS];
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
-        uint4 w[SETS];
         const float(&x0)[2] = x[2 * k];
         const float(&x1)[2] = x[2 * k + 1];
         if constexpr (!BF) {
-          w[0] = make_uint4(half_piece(x0[0], x0[1], 0), half_piece(x0[0], x0[1], 1), half_piece(x1[0], x1[1], 0),
-                            half_piece(x1[0], x1[1], 1));
+          w[k][0] = make_uint4(half_piece(x0[0], x0[1], 0), half_piece(x0[0], x0[1], 1), half_piece(x1[0], x1[1], 0),
+                               half_piece(x1[0], x1[1], 1));
         } else {
           uint32_t piece[3][2];
 #pragma unroll
@@ -379,37 +402,51 @@ struct MatrixLanes {
           }
           if constexpr (ROWS == 4) {
             const bool low = g < 4;  // rows 0-3 and 8-11: pieces 0 and 2; rows 4-7: piece 1
-            w[0] = make_uint4(low ? piece[0][0] : piece[1][0], low ? piece[2][0] : 0u,
-                              low ? piece[0][1] : piece[1][1], low ? piece[2][1] : 0u);
+            w[k][0] = make_uint4(low ? piece[0][0] : piece[1][0], low ? piece[2][0] : 0u,
+                                 low ? piece[0][1] : piece[1][1], low ? piece[2][1] : 0u);
           } else {
-            w[0] = make_uint4(piece[0][0], piece[1][0], piece[0][1], piece[1][1]);
-            w[SETS - 1] = make_uint4(piece[2][0], 0u, piece[2][1], 0u);
+            w[k][0] = make_uint4(piece[0][0], piece[1][0], piece[0][1], piece[1][1]);
+            w[k][SETS - 1] = make_uint4(piece[2][0], 0u, piece[2][1], 0u);
           }
         }
+      }
+      // A tile's products begin at zero and are added here: the matrix pipe cuts
+      // its sums off instead of rounding them, which over a warp's thousands of
+      // slots of one sign came to 1.4e-5 of the result.
 #pragma unroll
-        for (int cc = 0; cc < NC; ++cc) {
-          if constexpr (I8) {
+      for (int cc = 0; cc < NC; ++cc) {
+        if constexpr (I8) {
 #pragma unroll
-            for (int q = 0; q < VE / 4; ++q) {
+          for (int q = 0; q < VE / 4; ++q) {
+            float c[4][4] = {};
+#pragma unroll
+            for (int k = 0; k < NT; ++k) {
               uint32_t s[4];
 #pragma unroll
               for (int n = 0; n < 4; ++n) s[n] = word(vx[4 * k + n][cc], q) ^ 0x80808080u;
               const uint32_t lo0 = prmt(s[0], s[1], 0x5140), hi0 = prmt(s[0], s[1], 0x7362);
               const uint32_t lo1 = prmt(s[2], s[3], 0x5140), hi1 = prmt(s[2], s[3], 0x7362);
-              mma16816<TYPE>(acc[cc * VE + 4 * q], w[0], code_pair(lo0, 0x4140), code_pair(lo1, 0x4140));
-              mma16816<TYPE>(acc[cc * VE + 4 * q + 1], w[0], code_pair(lo0, 0x4342), code_pair(lo1, 0x4342));
-              mma16816<TYPE>(acc[cc * VE + 4 * q + 2], w[0], code_pair(hi0, 0x4140), code_pair(hi1, 0x4140));
-              mma16816<TYPE>(acc[cc * VE + 4 * q + 3], w[0], code_pair(hi0, 0x4342), code_pair(hi1, 0x4342));
+              mma16816<TYPE>(c[0], w[k][0], code_pair(lo0, 0x4140), code_pair(lo1, 0x4140));
+              mma16816<TYPE>(c[1], w[k][0], code_pair(lo0, 0x4342), code_pair(lo1, 0x4342));
+              mma16816<TYPE>(c[2], w[k][0], code_pair(hi0, 0x4140), code_pair(hi1, 0x4140));
+              mma16816<TYPE>(c[3], w[k][0], code_pair(hi0, 0x4342), code_pair(hi1, 0x4342));
             }
-          } else {
 #pragma unroll
-            for (int j = 0; j < VE; ++j) {
-              const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
+            for (int j = 0; j < 4; ++j) add(acc[cc * VE + 4 * q + j], c[j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
+            float c[4] = {};
+#pragma unroll
+            for (int k = 0; k < NT; ++k) {
               const uint32_t b0 = prmt(word(vx[4 * k][cc], j / 2), word(vx[4 * k + 1][cc], j / 2), sel);
               const uint32_t b1 = prmt(word(vx[4 * k + 2][cc], j / 2), word(vx[4 * k + 3][cc], j / 2), sel);
 #pragma unroll
-              for (int s = 0; s < SETS; ++s) mma16816<TYPE>(acc[cc * VE + j], w[s], b0, b1);
+              for (int s = 0; s < SETS; ++s) mma16816<TYPE>(c, w[k][s], b0, b1);
             }
+            add(acc[cc * VE + j], c);
           }
         }
       }
@@ -426,7 +463,7 @@ struct MatrixLanes {
     for (int i = 0; i < NC * VE; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float v = joined(acc[i][e], acc[i][2 + e]) * unit;
+        const float v = over_lanes(acc[i][e]) * unit;
         const int d = (2 * t + e + 8 * (i / VE)) * VE + i % VE;
         if (g < ROWS && d < D) to[head * D + d] = v;
       }

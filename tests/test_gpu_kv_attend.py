@@ -484,3 +484,40 @@ def test_attend_int8_scales_of_slots_that_add_nothing(where, group, dim, room):
         bound = tw[i] @ np.abs(v[:, h]) + 127 * n * 2.0 ** -44 * (w[i] * s[:, h]).max()
         off = np.abs(out[i] - ro[i])
         assert np.all(off <= bound), f"head {i}: off by {np.max(off / bound):.3g} bounds, {np.max(off) / np.abs(ro[i]).max():.3g} of the result"
+
+
+@pytest.mark.parametrize("kind,group", [("bfloat16", 1), ("bfloat16", 4), ("bfloat16", 8), ("float16", 8), ("int8", 8),
+                                        ("float32", 8)])
+def test_attend_long_sums_of_one_sign_have_no_bias(kind, group):
+    """Values of one sign over 65536 slots, about 2400 of them to a warp.
+
+    Sums rounded to nearest are off to either side: a row's by a walk of at most
+    1200 steps (a lane's weights; its values' tiles are fewer) of 2^-24, so by
+    2.1e-6 in a row's standard deviation at most, and 9.2e-8 in the mean over the
+    512 query heads here; ten of those are the bound, 2^-20. Cut off instead of
+    rounded, each step would lose 2^-25 and more of the sum to one side."""
+    T = torch()
+    rng = T.Generator("cuda").manual_seed(3)
+    B, H, n, D, page = 8, 8, 65536, 64, 64
+    P, dt = n // page, getattr(T, kind)
+    scales = (None, None)
+    if kind == "int8":
+        k, v = (T.randint(lo, 128, (P, H, page, D), generator=rng, device="cuda", dtype=T.int8) for lo in (-127, 40))
+        scales = [T.rand((P, H, page), generator=rng, device="cuda") * 0.01 + 0.01 for _ in range(2)]
+    else:
+        k = T.randn((P, H, page, D), generator=rng, device="cuda").to(dt)
+        v = (T.rand((P, H, page, D), generator=rng, device="cuda") + 0.5).to(dt)
+    table = T.randperm(P, generator=rng, device="cuda").to(T.int32)
+    cache = w4().KvCache(k, v, table.view(1, P).expand(B, P), T.full((B,), n, dtype=T.int32, device="cuda"), *scales)
+    q = T.randn((B, H * group, D), generator=rng, device="cuda")
+    out = w4().kv_attend(q, cache).double().view(B, H, group, D)
+    off = []
+    for h in range(H):
+        kk, vv = (x[table.long(), h].double() * (1 if s is None else s[table.long(), h].double()[..., None])
+                  for x, s in zip((k, v), scales))
+        kk, vv = kk.reshape(n, D), vv.reshape(n, D)
+        p = T.softmax(q.view(B, H, group, D)[:, h].double() @ kk.T * D ** -0.5, -1)
+        off.append(out[:, h] / (p @ vv) - 1)
+    off = T.stack(off)
+    assert abs(float(off.mean())) <= 2.0 ** -20, float(off.mean())
+    assert float(off.abs().max()) <= 2.0 ** -16

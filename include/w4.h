@@ -596,7 +596,8 @@ typedef struct kv_cache {
  * - lengths_out: int32 [seqs], lengths[b] + the rows given (the capacity at
  *   most). It may be the cache's own lengths (they advance in place) or
  *   memory apart from them. Rows beyond the capacity are not written and
- *   record W4_ERR_VALUE.
+ *   record W4_ERR_VALUE. So do the rows of a sequence whose length is below
+ *   0, which stays as it is.
  * A row of W4_KV_I8 that holds an Inf or NaN reads back as NaN. */
 W4_API w4_status kv_append(const kv_cache* c, const float* k, int64_t ldk, const float* v, int64_t ldv,
                            const int32_t* cu_tokens, int64_t tokens, int32_t* lengths_out, void* stream);

@@ -103,9 +103,16 @@ __device__ __forceinline__ int32_t rows_of(const AppendParams& p, int32_t b) {
   return n < 0 ? 0 : static_cast<int32_t>(min(n, int64_t(0x3fffffff)));
 }
 
+// Where a sequence's rows begin: its length. One below 0 (recorded) is no
+// place: it takes no rows, and stays.
+__device__ __forceinline__ int32_t start_of(const AppendParams& p, int32_t b) {
+  const int32_t n = p.c.lengths[b], held = held_length(p.c, b, p.err, w4dev::K_KV_APPEND);
+  return n < 0 ? n : held;
+}
+
 __device__ __forceinline__ int32_t advanced(const AppendParams& p, int32_t b) {
-  const int32_t n = held_length(p.c, b, p.err, w4dev::K_KV_APPEND) + rows_of(p, b);
-  return n > p.c.capacity ? p.c.capacity : n;
+  const int32_t n = start_of(p, b);
+  return n < 0 ? n : min(n + rows_of(p, b), p.c.capacity);
 }
 
 // The sequence whose rows hold row t: how many of cu[1..seqs] are <= t, by
@@ -277,17 +284,21 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     p.lengths_out[b_of_thread] = advanced(p, static_cast<int32_t>(b_of_thread));
   int32_t b = static_cast<int32_t>(t), slot = 0;
   if (p.cu == nullptr) {
-    if (t < p.tokens) slot = held_length(c, b, p.err, w4dev::K_KV_APPEND);
+    if (t < p.tokens) slot = start_of(p, b);
     __syncthreads();  // these threads alone read lengths[b], so it may be advanced in place
-    if (t < p.tokens && tid == 0) p.lengths_out[b] = min(slot + 1, c.capacity);
+    if (t < p.tokens && tid == 0) p.lengths_out[b] = slot < 0 ? slot : min(slot + 1, c.capacity);
   }
   if (t >= p.tokens) return;
   if (p.cu != nullptr) {
     b = sequence_of(p, t);
     if (b >= c.seqs || p.cu[b] > t || p.cu[b + 1] <= t) return;  // a row of no sequence
-    const int64_t at = held_length(c, b, p.err, w4dev::K_KV_APPEND) + (t - max(p.cu[b], 0));
-    slot = static_cast<int32_t>(at < c.capacity ? at : c.capacity);
+    slot = start_of(p, b);
+    if (slot >= 0) {
+      const int64_t at = slot + (t - max(p.cu[b], 0));
+      slot = static_cast<int32_t>(at < c.capacity ? at : c.capacity);
+    }
   }
+  if (slot < 0) return;
   if (slot >= c.capacity) {
     if (tid == 0) w4dev::record_error(p.err, W4_ERR_VALUE, w4dev::K_KV_APPEND, b);
     return;

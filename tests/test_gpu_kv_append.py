@@ -248,3 +248,32 @@ def test_append_refusals():
     shared = w4().KvCache(cache.k, cache.v, cache.page_table[:1].expand(2, 1), cache.lengths)
     with pytest.raises(w4().W4Error):
         w4().kv_append(shared, x, x)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("form", ["one each", "one each, elsewhere", "prompts", "prompts, elsewhere"])
+def test_append_to_a_negative_length_writes_nothing(kind, form):
+    """A length below 0 is no place: its sequence's rows are not written, the
+    length stays as it is, the error word says so; others advance."""
+    T = torch()
+    rng = np.random.default_rng(21)
+    cache, _, _ = build(rng, kind, [20, 20, 20], 2, 32, 16)
+    start = [-1, 4, -2 ** 31]
+    cache.lengths.copy_(T.tensor(start, dtype=T.int32))
+    x = rng.standard_normal((3, 2, 32)).astype(np.float32)
+    d = T.from_numpy(x).cuda()
+    stores = [t for t in (cache.k, cache.v, cache.k_scales, cache.v_scales) if t is not None]
+    before = [t.clone() for t in stores]
+    cu = T.tensor([0, 1, 2, 3], dtype=T.int32, device="cuda") if "prompts" in form else None
+    out = T.full((3,), 77, dtype=T.int32, device="cuda") if "elsewhere" in form else None
+    clear_error()
+    got = w4().kv_append(cache, d, d, cu_tokens=cu, lengths_out=out)
+    assert error_status() == 8
+    assert got.tolist() == [-1, 5, -2 ** 31]
+    assert cache.lengths.tolist() == (start if out is not None else got.tolist())
+    p = int(cache.page_table[1, 0])
+    s = None if cache.k_scales is None else cache.k_scales[p, :, 4].cpu().numpy()
+    assert np.array_equal(oracle.kv_values(cache.k[p, :, 4].float().cpu().numpy(), s), as_stored(x[1], kind))
+    for t, b in zip(stores, before):
+        t[p, :, 4] = b[p, :, 4]
+        assert T.equal(t.view(T.uint8), b.view(T.uint8))

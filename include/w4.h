@@ -635,7 +635,9 @@ W4_API w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, int64
 /* Cuts each sequence to at most `keep` slots: the last min(recent, keep) of
  * them, and of the rest those with the largest acc[b, j] (ties to the lower
  * slot; NaN ranks below everything). The kept slots move to the front, in
- * their order. A sequence of at most `keep` slots keeps all of them.
+ * their order. A sequence of at most `keep` slots keeps all of them. Of the
+ * slots to be kept, those whose page id names no page are dropped (and record
+ * W4_ERR_VALUE): the others close up, and the length counts them alone.
  * - src: the cache; acc: fp32 rows as kv_attend gathers them.
  * - dst: where the kept slots go: the same descriptor's arrays (in place: k,
  *   v, scales, page_table and lengths all equal), or a cache of the same

@@ -9,7 +9,8 @@
 // the adding threads wait for (16 sequences of up to 16000 slots: 24 us), and
 // two passes tell most thresholds apart. Ties at it stay from the lowest slot
 // on. Then each thread places four neighbouring slots behind the kept ones
-// before them: the kept slots' list.
+// before them: the kept slots' list. Slots on pages that do not exist leave it
+// again, in a pass of their own that only broken page tables bring about.
 // move_kernel: the kept rows of keys, values and scales to the front. A CTA
 // looks up the places of its rows once and moves them for several heads, the
 // next head's rows on their way while one's are written. Row i comes from slot
@@ -82,6 +83,8 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictParams p, in
   __shared__ uint32_t coarse[2][32];  // each warp's digits', of this CTA
   __shared__ uint32_t picked[5];      // see below
   __shared__ uint32_t warp_counts[2][32];
+  __shared__ int32_t broken;  // of the first CTA: whether a page id of the sequence names no page
+  if (threadIdx.x == 0) broken = 0;
   pdl_launch_dependents();
   pdl_wait();
   cg::cluster_group cluster = cg::this_cluster();
@@ -106,11 +109,18 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictParams p, in
     fresh = p.d.capacity;
   }
   const int32_t first = rank * THREADS + tid, step = ranks * THREADS;
+  const int32_t* table = p.c.table + b * p.c.ldp;
+  const auto no_page = [&](int32_t id) { return id < 0 || id >= p.c.num_pages; };
+  bool bad = false;
+  int32_t id = p.c.num_pages - 1;  // looked at last, when it has long arrived
   if (n <= p.keep) {
+    const int32_t pages = n > 0 ? p.c.page.quotient(n - 1) + 1 : 0;
+    for (int32_t i = first; i < pages; i += step) bad = bad || no_page(table[i]);
     for (int32_t i = first; i < fresh; i += step) {
       list[i] = i;
       if (acc_out != acc) acc_out[i] = acc[i];
     }
+    sync_all();  // `broken` is 0 from here on
   } else {
     const int32_t recent = min(p.recent, p.keep);
     const int32_t m = n - recent;          // the slots that compete
@@ -122,6 +132,9 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictParams p, in
     const auto weight = [&](int32_t i) { return held ? weights[i - c0] : acc[i]; };
     *reinterpret_cast<uint4*>(&hist[0][4 * tid]) = make_uint4(0, 0, 0, 0);
     __syncthreads();
+    // the first page ids are on their way while the weights are read
+    const int32_t page0 = p.c.page.quotient(c0), pages = c1 > c0 ? p.c.page.quotient(c1 - 1) - page0 + 1 : 0;
+    if (tid < pages) id = table[page0 + tid];
     constexpr int kAhead = 8;
     for (int32_t i0 = c0 + tid; i0 < c1; i0 += kAhead * THREADS) {
       float w[kAhead];
@@ -134,6 +147,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictParams p, in
         if (i < m1) atomicAdd(&hist[0][weight_key(w[j]) >> (32 - kBits)], 1u);
       }
     }
+    for (int32_t i = tid + THREADS; i < pages; i += THREADS) bad = bad || no_page(table[page0 + i]);
     if (none) sync_all();
     uint32_t prefix = 0;
     uint32_t sure_before = max(0, c0 - m), at_before = 0;  // of the CTAs before: slots that stay for sure, and at the threshold
@@ -276,9 +290,36 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictParams p, in
   }
   for (int32_t i = fresh + first; i < n; i += step) acc_out[i] = 0.f;
   for (int32_t i = fresh + first; i < p.pad; i += step) list[i] = -1;
+  if (bad || no_page(id)) *cluster.map_shared_rank(&broken, 0) = 1;
   // the length changes once all of the cluster have read it
   sync_all();
-  if (rank == 0 && tid == 0) p.d.lengths[b] = fresh;
+  if (rank != 0) return;
+  if (broken != 0) {  // kept slots without a page count as empty: the others close up
+    int32_t m = 0;
+    int turn = 0;
+    for (int32_t i0 = 0; i0 < fresh; i0 += THREADS, turn ^= 1) {
+      const int32_t i = i0 + tid, slot = i < fresh ? __ldcg(list + i) : 0;
+      const float w = i < fresh ? __ldcg(acc_out + i) : 0.f;
+      const bool stays = i < fresh && page_of(p.c, b, p.c.page.quotient(slot), p.err, w4dev::K_KV_EVICT) >= 0;
+      const uint32_t votes = __ballot_sync(0xffffffffu, stays);
+      if (lane == 0) warp_counts[turn][warp] = __popc(votes);
+      __syncthreads();  // and all of this tile has been read
+      const uint32_t wc = lane < kWarps ? warp_counts[turn][lane] : 0u;
+      const int32_t at = m + __reduce_add_sync(0xffffffffu, lane < warp ? wc : 0u) + __popc(votes & ((1u << lane) - 1u));
+      if (stays) {
+        list[at] = slot;
+        acc_out[at] = w;
+      }
+      m += __reduce_add_sync(0xffffffffu, wc);
+    }
+    __syncthreads();
+    for (int32_t i = m + tid; i < fresh; i += THREADS) {
+      acc_out[i] = 0.f;
+      if (i < p.pad) list[i] = -1;
+    }
+    fresh = m;
+  }
+  if (tid == 0) p.d.lengths[b] = fresh;
 }
 
 // Where slot `slot`'s row of head 0 lies: its number among the rows of k and v,

@@ -166,3 +166,59 @@ def test_evict_refusals():
     shared = W.KvCache(free.k, free.v, free.page_table[:1].expand(2, 2), free.lengths)
     with pytest.raises(W.W4Error):
         W.kv_evict(cache, acc, 3, dst=shared, acc_out=T.zeros((2, 32), device="cuda"))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("lengths,keep,recent", [([100, 40, 64], 50, 10), ([100, 40, 64], 300, 0), ([100, 40, 64], 20, 20),
+                                                 ([9000, 40, 70], 3000, 200), ([150003], 20011, 5000)])
+def test_evict_drops_kept_slots_of_broken_pages(kind, in_place, lengths, keep, recent):
+    """Slots whose page id names no page count as empty: none is kept, what is
+    kept closes up, and the length counts that alone."""
+    T = torch()
+    if len(lengths) == 1 and kind in ("float32", "float16"):
+        pytest.skip("the long sequence once for 16 bits, once with scales")
+    rng = np.random.default_rng(len(lengths) * 10 + keep)
+    page, heads, dim = 16, 1 if max(lengths) > 1000 else 2, 16
+    cache, k, v = build(rng, kind, lengths, heads, dim, page)
+    acc = weights(rng, lengths, cache.capacity)
+    B, table = len(lengths), cache.page_table.cpu().numpy()
+    bad = {0: [3, 5, lengths[0] // page], 1: [0]}  # of sequence 0 the last one too; sequence 2 is whole
+    if B == 1:
+        bad = {0: [1, 700, 9000, lengths[0] // page]}
+    for b, pages in bad.items():
+        for i, p in enumerate(pages):
+            cache.page_table[b, p] = (-1, cache.k.shape[0], 2 ** 31 - 1, -2 ** 31)[i]
+    accd = T.from_numpy(acc).cuda()
+    kept = T.full((B, keep + 1), 77, dtype=T.int32, device="cuda")
+    dst = None
+    if not in_place:
+        dst, _, _ = build(rng, kind, [min(n, keep) for n in lengths], heads, dim, page)
+    for with_kept in (True, False):
+        if not with_kept and in_place:
+            break  # the cache has been cut
+        acc_out = accd if in_place else T.full((B, cache.capacity), 5.0, device="cuda")
+        clear_error()
+        got = w4().kv_evict(cache, accd, keep, recent=recent, dst=dst, acc_out=acc_out, kept=kept if with_kept else None)
+        assert error_status() == 8
+        want = []
+        for b, n in enumerate(lengths):
+            j = np.array(oracle.kv_evict_ref(acc[b], n, keep, recent))
+            want.append(j[~np.isin(j // page, bad.get(b, []))])
+        assert got.tolist() == [len(j) for j in want]
+        to = dst if dst is not None else cache
+        to_table = to.page_table.cpu().numpy()
+        kc, ao = kept.cpu().numpy(), acc_out.cpu().numpy()
+        for b, j in enumerate(want):
+            n, m = lengths[b], len(j)
+            if with_kept:
+                assert np.array_equal(kc[b, :m], j) and np.all(kc[b, m:keep] == -1) and np.all(kc[b, keep:] == 77)
+            assert np.array_equal(ao[b, :m], acc[b, j]) and np.all(ao[b, m:n] == 0)
+            assert np.all(ao[b, n:] == (0 if in_place else 5.0))
+            r = np.arange(m)
+            there = r if not in_place else r[~np.isin(r // page, bad.get(b, []))]  # in place the broken pages hold nothing
+            p = to_table[b, there // page]
+            for t, sc, rows in ((to.k, to.k_scales, k), (to.v, to.v_scales, v)):
+                x = t.cpu().double().numpy()[p, :, there % page]
+                s = None if sc is None else sc.cpu().numpy()[p, :, there % page]
+                assert np.array_equal(oracle.kv_values(x, s), rows[b][j[there]]), b

@@ -222,3 +222,27 @@ def test_evict_drops_kept_slots_of_broken_pages(kind, in_place, lengths, keep, r
                 x = t.cpu().double().numpy()[p, :, there % page]
                 s = None if sc is None else sc.cpu().numpy()[p, :, there % page]
                 assert np.array_equal(oracle.kv_values(x, s), rows[b][j[there]]), b
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n", [9000, 40000, 150003])
+@pytest.mark.parametrize("steps", [1, 4, 0])
+def test_evict_ties_over_a_cluster(in_place, n, steps):
+    """A threshold that many slots of several CTAs share, of which only part
+    stay: few different weights, and all alike."""
+    rng = np.random.default_rng(n + steps)
+    cap = -(-n // 16) * 16
+    acc = np.zeros((1, cap), np.float32)
+    if steps:
+        acc[0, :n] = np.floor(rng.random(n) * (steps + 1))
+    for keep, recent in ((n // 3, 100), (n - 5, 0), (n // 2, n // 2)):
+        run("bfloat16", [n], keep, recent, heads=1, dim=16, in_place=in_place, acc=acc, seed=n)
+
+
+@pytest.mark.parametrize("kind,heads", [("int8", 3), ("float32", 4), ("bfloat16", 5)])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("recent", [0, 1200, 5000])
+def test_evict_many_rows_of_several_heads(kind, heads, in_place, recent):
+    """More rows than a batch, of several heads and with scales; recent >= keep
+    asks nothing of the weights."""
+    run(kind, [5000, 9000, 1100, 1201], 1200, recent, heads, 64, 16, in_place, seed=recent + heads)

@@ -622,8 +622,10 @@ W4_API w4_status kv_append(const kv_cache* c, const float* k, int64_t ldk, const
  *   2^35 (group: q_heads / kv_heads); one far above it is W4_ERR_SHAPE.
  * - scale: finite, below 2^127 in magnitude.
  * Sums and the softmax are fp32; K and V enter with their stored values. A
- * NaN or Inf in q or in an attended slot makes the rows that it reaches
- * non-finite; what lies in other slots has no effect. The weighted values are
+ * NaN or Inf in q or in an attended key, or a score beyond fp32's range of
+ * either sign, makes the query head's whole row, its lse and what acc gains
+ * from it non-finite; one in an attended value the elements that it is added
+ * to. What lies in other slots has no effect. The weighted values are
  * summed before they are divided, with weights of up to 2^7 (fp16: 2^14):
  * stored values beyond 2^96 may overflow there. Results do not depend
  * on timing: the same call gives the same bits. */

@@ -91,8 +91,8 @@ __device__ __forceinline__ void join_heads(const AttendParams& p, int wpr) {
 
 // The query heads' log sums to base 2, 32 heads at a time by 8 lanes each: as
 // the attention kernel wrote them, or from the partials, so that the weights
-// need not wait for the join. -Inf: every attended score is -Inf, and weighs
-// nothing.
+// need not wait for the join. -Inf: none of the attended slots is there (all on
+// pages that do not exist), and nothing weighs anything.
 __device__ __forceinline__ void log_sums(const AttendParams& p, int32_t b, int32_t q0, int heads, bool runs, float* z) {
   const int sub = threadIdx.x % 8;
   for (int i0 = 0; i0 < heads; i0 += kJoinThreads / 8) {

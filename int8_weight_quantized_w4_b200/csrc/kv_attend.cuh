@@ -284,6 +284,10 @@ struct Queries {
   }
 };
 
+// A score as it is, or NaN for an infinite one: of a key with an Inf the bodies'
+// products are an Inf of either sign or a NaN, and -Inf would weigh nothing.
+__device__ __forceinline__ float finite(float x) { return fmaf(x, 0.f, x); }
+
 // (a, m, l) of one quad of a query head's sums.
 struct Triple {
   float4 a;
@@ -712,7 +716,7 @@ struct PlainLanes {
         float f = p.scale2;
         if constexpr (TYPE == W4_KV_I8) f *= scales[i * RPW + rg];
 #pragma unroll
-        for (int g = 0; g < GT; ++g) x[g][i] *= f;
+        for (int g = 0; g < GT; ++g) x[g][i] = finite(x[g][i] * f);
       }
       if (held != Feed::kAll) {
 #pragma unroll

@@ -291,8 +291,8 @@ struct MatrixLanes {
       for (int n = 0; n < 2 * NT; ++n) {
         float2 f = make_float2(1.f, 1.f);
         if constexpr (I8) f = *reinterpret_cast<const float2*>(scales + 8 * n + 2 * t);
-        x[n][0] = joined(c[n][0], c[n][2]) * (scale * f.x);
-        x[n][1] = joined(c[n][1], c[n][3]) * (scale * f.y);
+        x[n][0] = finite(joined(c[n][0], c[n][2]) * (scale * f.x));
+        x[n][1] = finite(joined(c[n][1], c[n][3]) * (scale * f.y));
       }
       if (held != Feed::kAll) {
 #pragma unroll

@@ -521,3 +521,32 @@ def test_attend_long_sums_of_one_sign_have_no_bias(kind, group):
     off = T.stack(off)
     assert abs(float(off.mean())) <= 2.0 ** -20, float(off.mean())
     assert float(off.abs().max()) <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("room", ROOMS)
+@pytest.mark.parametrize("kind", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("group,dim", [(1, 64), (2, 64), (4, 128), (8, 64), (5, 192)])
+def test_attend_infinite_keys_reach_their_rows(kind, group, dim, room):
+    """An Inf in an attended key makes every row of its key-value head
+    non-finite, with weights and log sums, whichever sign the score has and
+    whichever body the sizes choose; every other row keeps its bits."""
+    T = torch()
+    rng = np.random.default_rng(43)
+    for n, most in (([700, 90, 33], 0), ([20, 90, 33], 8)):  # the second: few slots, the plain lanes for any group
+        cache, k, v = build(rng, kind, n, 2, dim, 16, max_pages=room_for(room, 16) or most or None)
+        q = rng.standard_normal((3, 2 * group, dim)).astype(np.float32)
+        q[0, :, 7] = np.where(np.arange(2 * group) % 2, 0.5, -0.5)  # scores of both signs
+        qd = T.from_numpy(q).cuda()
+        lse0, acc0 = T.empty((3, 2 * group), device="cuda"), T.zeros((3, cache.capacity), device="cuda")
+        base = w4().kv_attend(qd, cache, lse=lse0, acc=acc0)
+        for at in (0, 13, n[0] - 1):
+            p = int(cache.page_table[0, at // 16])
+            was = float(cache.k[p, 1, at % 16, 7])
+            cache.k[p, 1, at % 16, 7] = float("inf")
+            lse, acc = T.empty_like(lse0), T.zeros_like(acc0)
+            out = w4().kv_attend(qd, cache, lse=lse, acc=acc)
+            cache.k[p, 1, at % 16, 7] = was
+            assert not T.isfinite(out[0, group:]).any() and not T.isfinite(lse[0, group:]).any()
+            assert not T.isfinite(acc[0, :n[0]]).any()
+            assert T.equal(out[0, :group], base[0, :group]) and T.equal(out[1:], base[1:])
+            assert T.equal(lse[0, :group], lse0[0, :group]) and T.equal(lse[1:], lse0[1:]) and T.equal(acc[1:], acc0[1:])

@@ -550,3 +550,23 @@ def test_attend_infinite_keys_reach_their_rows(kind, group, dim, room):
             assert not T.isfinite(acc[0, :n[0]]).any()
             assert T.equal(out[0, :group], base[0, :group]) and T.equal(out[1:], base[1:])
             assert T.equal(lse[0, :group], lse0[0, :group]) and T.equal(lse[1:], lse0[1:]) and T.equal(acc[1:], acc0[1:])
+
+
+@pytest.mark.parametrize("room", ROOMS)
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("heads,group,dim", [(3, 1, 64), (2, 2, 96), (2, 5, 128), (1, 8, 64), (1, 4, 256)])
+def test_attend_queries_at_any_address(kind, heads, group, dim, room):
+    """Rows of queries that begin at 4-byte addresses, an odd distance apart:
+    runs, clusters and warps' items."""
+    T = torch()
+    rng = np.random.default_rng(heads * 7 + group + dim)
+    for lengths, pages in (([0, 1, 17, 130, 700], room_for(room, 16)), ([int(x) for x in rng.integers(0, 50, 900)], 4)):
+        cache, k, v = build(rng, kind, lengths, heads, dim, 16, max_pages=pages)
+        B, W = len(lengths), heads * group * dim
+        q = rng.standard_normal((B, heads * group, dim)).astype(np.float32)
+        wide = T.full((B, W + 41), float("nan"), device="cuda")
+        wide[:, 9:9 + W] = T.from_numpy(q.reshape(B, W)).cuda()
+        odd = wide[:, 9:9 + W].view(B, heads * group, dim)
+        assert odd.data_ptr() % 16 and odd.stride(0) % 4
+        out = w4().kv_attend(odd, cache)
+        assert T.equal(out, check(cache, k, v, q, what=f"{kind} {heads}x{group}x{dim}"))

@@ -35,10 +35,20 @@ constexpr int kSelSmall = 256;      // for sequences of up to kSmall slots: 9 us
 constexpr int kSmall = 2048;
 constexpr int kMaxRanks = 8;        // CTAs of a selecting cluster
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 4;
-constexpr int kMoveCtas = 4;        // CTAs an SM that the heads are shared out for
-constexpr int kShare = 4160;       // slots that a sequence grows by another CTA at
+// CTAs an SM that the heads are shared out for: one sequence of 131072 slots, 8 x
+// 128 bf16, cut to 8192, 29.3 us (with 2 28.5 us, with 8 31.1 us); one of 5000, 12 x
+// 64 fp32, 15.2 us (15.9 us, 15.2 us).
+constexpr int kMoveCtas = 4;
+// Slots that a sequence grows by another CTA at: 16 of up to 16000 slots 52.1 us
+// (with 2080 54.4 us, with 8320 53.8 us); one of 8000 17.6 us (17.1 us, 18.5 us).
+constexpr int kShare = 4160;
 constexpr int kHeld = 16640;        // weights that a selecting CTA keeps in shared memory
+
+// Rows of a moving thread at a time. In place a batch is read as a whole before
+// it is written, and int8 rows are short: 4 (16 x <= 16000 slots of 128 bf16 in place
+// 58 us, 66 us with 2; int8 into other pages 39.5 us, 41 us); else 2 (64 x <= 2000
+// fp16 73 us, 75.5 us with 4; one 12 x 64 sequence of 1024 8.0 us, 9.1 us).
+constexpr int move_unroll(bool in_place, bool scales) { return in_place || scales ? 4 : 2; }
 
 struct EvictParams {
   View c, d;
@@ -335,10 +345,10 @@ __device__ __forceinline__ uint32_t row_of(const View& c, int32_t b, int32_t slo
 }
 
 // A batch's rows of one head's keys or values.
-template <bool SCALES>
+template <int ROWS, bool SCALES>
 struct Batch {
-  uint4 x[kMoveUnroll];
-  float s[SCALES ? kMoveUnroll : 1];
+  uint4 x[ROWS];
+  float s[SCALES ? ROWS : 1];
 };
 
 // vecs: 16-byte vectors of a row; per: those of this CTA's columns; in place
@@ -346,6 +356,8 @@ struct Batch {
 // of `group` heads.
 template <bool IN_PLACE, bool SCALES>
 __global__ void __launch_bounds__(kMoveThreads, 3) move_kernel(const EvictParams p, int vecs, int per, int group) {
+  constexpr int kRows = move_unroll(IN_PLACE, SCALES);
+  using Rows = Batch<kRows, SCALES>;
   pdl_launch_dependents();
   pdl_wait();
   const int32_t b = blockIdx.z;
@@ -356,21 +368,21 @@ __global__ void __launch_bounds__(kMoveThreads, 3) move_kernel(const EvictParams
   const int width = min(per, vecs - column);
   const int stride = kMoveThreads / width;
   const int my_row = threadIdx.x / width, my_vec = column + threadIdx.x % width;
-  const int rows = stride * kMoveUnroll;  // of a batch
+  const int rows = stride * kRows;  // of a batch
   const bool live = my_row < stride;
   const bool scales = SCALES && my_vec == 0;
   int32_t r0 = IN_PLACE ? 0 : static_cast<int32_t>(min(int64_t(fresh), int64_t(blockIdx.x) * rows));
   const int32_t end = IN_PLACE ? fresh : min(fresh, r0 + rows);
   for (; r0 < end; r0 += rows) {
-    uint32_t from[kMoveUnroll], to[kMoveUnroll], from_scale[kMoveUnroll], to_scale[kMoveUnroll];
-    int32_t slot[kMoveUnroll];
+    uint32_t from[kRows], to[kRows], from_scale[kRows], to_scale[kRows];
+    int32_t slot[kRows];
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
+    for (int u = 0; u < kRows; ++u) {
       const int32_t r = r0 + u * stride + my_row;
       slot[u] = live && r < end ? list[r] : -1;
     }
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
+    for (int u = 0; u < kRows; ++u) {
       const int32_t r = r0 + u * stride + my_row;
       from_scale[u] = to_scale[u] = 0;
       from[u] = to[u] = kNoRow;
@@ -382,31 +394,31 @@ __global__ void __launch_bounds__(kMoveThreads, 3) move_kernel(const EvictParams
     }
     // step i: keys of heads h0 .. h1 - 1, then their values
     const auto head = [&](int i) { return i < h1 - h0 ? h0 + i : i - (h1 - h0) + h0; };
-    const auto load = [&](Batch<SCALES>& x, int i) {
+    const auto load = [&](Rows& x, int i) {
       const uint32_t h = head(i) * p.c.slots_per_page;
       const uint4* src = static_cast<const uint4*>(i < h1 - h0 ? p.c.k : p.c.v) + my_vec;
       const float* ss = i < h1 - h0 ? p.c.ks : p.c.vs;
 #pragma unroll
-      for (int u = 0; u < kMoveUnroll; ++u) {
+      for (int u = 0; u < kRows; ++u) {
         if (to[u] != kNoRow) {
           x.x[u] = src[uint64_t(from[u] + h) * vecs];
           if (scales) x.s[u] = ss[from_scale[u] + h];
         }
       }
     };
-    const auto store = [&](const Batch<SCALES>& x, int i) {
+    const auto store = [&](const Rows& x, int i) {
       const uint32_t h = head(i) * p.c.slots_per_page;
       uint4* dst = static_cast<uint4*>(i < h1 - h0 ? p.d.k : p.d.v) + my_vec;
       float* ds = i < h1 - h0 ? p.d.ks : p.d.vs;
 #pragma unroll
-      for (int u = 0; u < kMoveUnroll; ++u) {
+      for (int u = 0; u < kRows; ++u) {
         if (to[u] != kNoRow) {
           dst[uint64_t(to[u] + h) * vecs] = x.x[u];
           if (scales) ds[to_scale[u] + h] = x.s[u];
         }
       }
     };
-    Batch<SCALES> even, odd;
+    Rows even, odd;
     const int count = 2 * (h1 - h0);  // even
     load(even, 0);
     for (int i = 0; i < count; i += 2) {
@@ -550,7 +562,7 @@ extern "C" w4_status kv_evict(const kv_cache* src, const float* acc, int64_t lda
   if (most == 0) return W4_OK;
   // heads of a CTA: as many as leave every SM a few CTAs
   const int per = in_place ? (vecs < 4 ? vecs : 4) : vecs;
-  const int rows = kMoveThreads / per * kMoveUnroll;
+  const int rows = kMoveThreads / per * move_unroll(in_place, src->type == W4_KV_I8);
   const int64_t pieces = in_place ? (vecs + per - 1) / per : (most + rows - 1) / rows;
   int group = src->kv_heads;
   while (group > 1 && pieces * src->seqs * ((src->kv_heads + group - 1) / group) < int64_t(kMoveCtas) * di->sms)

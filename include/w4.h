@@ -592,7 +592,8 @@ typedef struct kv_cache {
  *   cu_tokens[b + 1] - 1 go to sequence b, the first to slot lengths[b].
  *   Rows of no sequence are left out. An entry below the one before it, or
  *   outside 0 .. tokens, records W4_ERR_VALUE; rows that are not there do not
- *   count. NULL: one row for each sequence (tokens == seqs).
+ *   count (entries out of order leave open which of their rows the sequences
+ *   concerned get). NULL: one row for each sequence (tokens == seqs).
  * - lengths_out: int32 [seqs], lengths[b] + the rows given (the capacity at
  *   most). It may be the cache's own lengths (they advance in place) or
  *   memory apart from them. Rows beyond the capacity are not written and
@@ -621,14 +622,20 @@ W4_API w4_status kv_append(const kv_cache* c, const float* k, int64_t ldk, const
  * - a call takes seqs * kv_heads * ceil(group / 2) * (capacity + 64) below
  *   2^35 (group: q_heads / kv_heads); one far above it is W4_ERR_SHAPE.
  * - scale: finite, below 2^127 in magnitude.
- * Sums and the softmax are fp32; K and V enter with their stored values. A
- * NaN or Inf in q or in an attended key, or a score beyond fp32's range of
+ * Sums and the softmax are fp32; K and V enter with their stored values. Where
+ * several query heads share a key-value head of an fp16 or int8 cache, the
+ * products take the query and the softmax weights to 22 bits: what is left out
+ * is below 2^-22 of each of them, or below 2^-50 of the head's largest query
+ * element and 2^-43 of its largest weight (int8: of its largest weight times
+ * scale), whichever is more. fp32 and bf16 caches, one query head a key-value
+ * head, and few slots take them whole.
+ * A NaN or Inf in q or in an attended key, or a score beyond fp32's range of
  * either sign, makes the query head's whole row, its lse and what acc gains
  * from it non-finite; one in an attended value the elements that it is added
- * to. What lies in other slots has no effect. The weighted values are
- * summed before they are divided, with weights of up to 2^7 (fp16: 2^14):
- * stored values beyond 2^96 may overflow there. Results do not depend
- * on timing: the same call gives the same bits. */
+ * to. What lies in other slots has no effect. The weighted values are summed
+ * before they are divided, with weights of up to 2^7 (fp16: 2^14): stored values
+ * beyond 2^96 may overflow there. Results do not depend on timing: the same
+ * call gives the same bits. */
 W4_API size_t kv_attend_workspace_size(const kv_cache* c, int64_t q_heads, int32_t with_acc);
 W4_API w4_status kv_attend(const kv_cache* c, const float* q, int64_t ldq, int64_t q_heads, float scale,
                            int64_t window, float* out, int64_t ldo, float* lse, float* acc, int64_t ldacc,

@@ -8,7 +8,9 @@
 // values are already on their way. int8 rows go to half-warps, 16 lanes of 4
 // elements wide, which a row's maximum is reduced over; the others are copied
 // as they come, 4 elements a thread. Measured: 7254 tokens of 32 x 96 to bf16
-// 45 us, 5.9 TB/s (0.92 of a plain copy); 8 tokens of 12 x 64 3.2 us.
+// 48.5 us, 5.5 TB/s (0.85 of a plain copy; 44.4 us where part of the rows lies in
+// L2), to int8 74.5 us: a half-warp has one further row on its way; 8 tokens of
+// 12 x 64 3.1 us.
 #include "kv_cache.cuh"
 
 namespace w4host {

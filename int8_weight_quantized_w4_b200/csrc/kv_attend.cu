@@ -26,8 +26,14 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kMostUnits = 16;
 constexpr int kShortUnits = 4;
-constexpr int kLeastSlots = 64;  // of a CTA in runs: fewer cost more to join than they save
-constexpr int kGatherCtas = 16;  // CTAs an SM that the weights are shared out for
+// Slots of a CTA in runs: fewer cost more to join than they save, more leave too
+// few CTAs. One sequence of 1000 slots, 2 x 128 fp32, in a table for 40000, 8.9 us
+// (with 16 9.9 us, with 256 13.6 us); of 6000 12.9 us (24.1 us, 15.5 us).
+constexpr int kLeastSlots = 64;
+// CTAs an SM that the weights are shared out for: 64 sequences of up to 2000 slots,
+// 8 x 128 bf16 for 32 heads, 61.7 us (with 4 62.8 us, with 64 62.9 us); 8 of up to
+// 4000, 32 x 96 fp16, 51.0 us (51.8 us, 51.0 us); one of 131072 119 us (110 us, 128 us).
+constexpr int kGatherCtas = 16;
 constexpr int kMaxLaneVecs = 2;  // float4s of a lane: 32 x 4 x 2 = 256, the largest head_dim
 
 // The partials of an item: its first one, then the next CTAs' first ones.
@@ -208,15 +214,15 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 // Brief: slots too few for the matrix body, whose staging of the queries is then
 // most of its time. Plain lanes against matrices, 8 key-value heads:
 //   a tile or two of slots, whatever the batch: 200 sequences of 32 slots of 256
-//     bf16 for 32 heads 32 us against 41 us, of 128 int8 16 us against 22 us (64
-//     slots: 26 us against 28 us; 32 of 64 bf16: 9.2 us against 6.7 us);
-//   little work: 4 x 300 slots of 128 fp16 for 32 heads 7.5 us against 9.7 us, for
-//     64 heads 8.5 us against 10.2 us (4 x 1000 for 64: 15.3 us against 11.5 us);
-//     int8 for 32 heads 4 x 1000 10.0 us against 14.1 us (16 x 1000: 24 us
-//     against 22 us).
+//     bf16 for 32 heads 29.6 us against 35.6 us, of 128 int8 16.3 us against 17.2 us
+//     (64 slots: 25.6 us against 20.6 us; 32 of 64 bf16: 9.1 us against 6.2 us);
+//   little work: 4 x 300 slots of 128 fp16 for 32 heads 7.5 us against 8.2 us, for
+//     64 heads 8.5 us against 8.8 us (4 x 1000 for 64: 15.4 us against 10.2 us);
+//     int8 for 32 heads 4 x 300 7.4 us against 9.6 us, 4 x 1000 10.0 us against
+//     11.2 us (16 x 1000: 24 us against 18 us).
 // Rows of more than 128 elements of 16 bits are many registers to a plain lane
-// (4 x 300 of 192 bf16 for 32 heads: 10 us against 8.7 us), and int8 rows of up to 64
-// are as fast in matrices (1 x 1000 for 32 heads: 6.8 us against 5.4 us).
+// (4 x 300 of 192 bf16 for 32 heads: 10.3 us against 7.9 us), and int8 rows of up to
+// 64 are faster in matrices (1 x 1000 for 32 heads: 6.9 us against 5.6 us).
 // slots: the most that a sequence attends.
 AttendKernel choose(const w4kv::View& c, int type, int32_t group, int64_t slots) {
   const bool i8 = type == W4_KV_I8;
@@ -311,10 +317,10 @@ w4_status lay_out(const w4kv::View& c, const AttendKernel& kernel, int64_t slots
   // An item a cluster: the widest of up to 16 CTAs that one wave holds for all
   // items, where it leaves a CTA kMostUnits units (of 64 slots at most) of a full
   // sequence: runs balance the CTAs, clusters save the second launch. One
-  // 12 x 64 fp32 sequence of 1021 slots: 5.5 us against 8.8 us as runs and a
-  // join; 48 of 1024, bf16: 26 us against 33 us; 8 of 1000, 8 x 128 bf16 for 32
-  // heads: 12.3 us against 16.1 us; twice the units, 48 of up to 2048, 33.5 us
-  // against 32.3 us; 32 of up to 2000, 8 x 128 int8 for 64 heads, 41 us against 37 us.
+  // 12 x 64 fp32 sequence of 1021 slots: 5.7 us against 9.0 us as runs and a
+  // join; 48 of 1024, bf16: 26 us against 32 us; 8 of 1000, 8 x 128 bf16 for 32
+  // heads: 11.1 us against 14.4 us; with more units, 48 of up to 2048, 32.3 us
+  // against 29.4 us; 32 of up to 2000, 8 x 128 int8 for 64 heads, 40 us against 31 us.
   // (As many as the GPCs hold, not as their SMs' sum does: 32 clusters of 16 are
   // one wave by the sum at 4 CTAs an SM, and took two.)
   int log = kRankLogs - 1;
@@ -322,8 +328,8 @@ w4_status lay_out(const w4kv::View& c, const AttendKernel& kernel, int64_t slots
   const int64_t most_slots = int64_t(kMostUnits) * std::min(64, L.kernel.unit) << log;
   L.ranks = items <= held.clusters[log] && slots <= most_slots ? 1u << log : 0;
   // More items than a wave of CTAs, and all of them short. 400 sequences of 64
-  // slots, 12 x 64 bf16: 17 us against 30 us in runs; 1000 of 100, fp16: 58 us
-  // against 80 us; 200 of 200, 8 x 128 bf16 for 32 heads: 47 us against 46 us.
+  // slots, 12 x 64 bf16: 13.7 us against 29 us in runs; 1000 of 100, fp16: 57 us
+  // against 79 us; 200 of 200, 8 x 128 bf16 for 32 heads: 46 us against 43 us.
   L.warps = L.ranks == 0 && items > wave && slots <= kShortUnits * L.kernel.unit;
   if (L.ranks != 0 || L.warps) {
     const int64_t by_warp = std::min((items + kWarps - 1) / kWarps, int64_t(held.warp_per_sm) * sms);

@@ -29,10 +29,11 @@
 // which also writes the zeros of slots that are not there), whichever segments
 // they belong to; their entries of the page table were fetched a tile earlier.
 //
-// Measured, call after call: 131072 slots of 8 x 128 bf16 for 32 query heads
-// 91 us, 5.9 TB/s of keys and values (0.91 of what a plain copy moves); 48
-// sequences of up to 1024 slots, 12 x 64 bf16, 19 us (4.0 TB/s); one of 1021
-// slots, 12 x 64 fp32, 5.6 us, bound by its chain of reads.
+// Measured, on the device: 131072 slots of 8 x 128 bf16 for 32 query heads
+// 90 us, 5.9 TB/s of keys and values (0.92 of what a plain copy moves); 48
+// sequences of up to 1024 slots, 12 x 64 bf16, 17.4 us (4.4 TB/s), of 1024 all
+// 26.1 us (5.8 TB/s); one of 1021 slots, 12 x 64 fp32, 5.7 us, bound by its chain
+// of reads.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -644,7 +645,8 @@ struct Ring {
 // a row's lanes leaves the score with each of them and the same lanes add the
 // row's values without an exchange; each group of LPR lanes carries its own
 // (m, l, a) and the groups join at the end. Tiles are 4 KB (K and V) or a
-// little less, whatever the rows: 16, 8 or 4 slots.
+// little less, 16, 8 or 4 slots; fp32 rows of more than 128 elements 6 or 8 KB,
+// 4 slots.
 template <int TYPE, int LPR, int VPL, int GT>
 struct PlainLanes {
   using E = Elem<TYPE>;

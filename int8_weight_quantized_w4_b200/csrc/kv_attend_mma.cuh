@@ -35,7 +35,7 @@
 // codes have to pass the registers anyway. Rate is not what is short: on
 // 131072 slots of 8 x 128 bf16 for 32 heads the tensor pipe is busy a fifth of
 // the time and DRAM delivers 6.1 TB/s; int8 (32 sequences of up to 4096 slots,
-// 8 x 128 for 64 heads: 58 us, 3.4 TB/s) is held by the conversions' dependent
+// 8 x 128 for 64 heads: 54 us, 3.6 TB/s) is held by the conversions' dependent
 // instructions at the 12 warps that an SM's registers hold.
 #pragma once
 
@@ -471,11 +471,12 @@ struct MatrixLanes {
   }
 };
 
-// Query heads of a key-value head from which on the matrices are faster, where
+// Query heads of a key-value head from which on the matrices are taken, where
 // there are slots enough. Two heads, 16 sequences of 4000 slots of 8 key-value heads:
-// 64 bf16 30 us in plain lanes, 33 us in matrices; 128 int8 43 us, 49 us; 160
-// bf16 101 us, 62 us; 256 int8 111 us, 76 us. Three heads, 8 sequences of 6000
-// slots of 16 x 128 bf16: 124 us, 70 us.
+// 160 bf16 101 us in plain lanes, 61 us in matrices; 256 int8 112 us, 65 us. Rows
+// of up to 128 gain little from them (64 bf16 29.4 us, 24.6 us; 128 int8 42.9 us,
+// 40.6 us) and keep the lanes' whole fp32 queries and weights. Three heads, 8
+// sequences of 6000 slots of 16 x 128 bf16: 123 us, 67 us.
 inline int32_t least_group(int32_t dim) { return dim > 128 ? 2 : 3; }
 
 // The matrix kernel for this many query heads, where there is one.

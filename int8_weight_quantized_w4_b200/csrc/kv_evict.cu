@@ -19,8 +19,9 @@
 // one CTA takes the batches of one 64-byte column in order, elsewhere batches
 // are dealt out.
 // Measured: 16 sequences of up to 16000 slots cut to 2045, 8 x 128 bf16 into
-// other pages, 52 us: 15 us to select, bound by its passes' barriers, and 37 us
-// to move, 6.2 TB/s; one 12 x 64 fp32 sequence of 1024 slots cut to 512, 8.5 us.
+// other pages, 51 us: 15 us to select, bound by its passes' barriers, and 36 us
+// to move, 6.3 TB/s; in place 57 us; one 12 x 64 fp32 sequence of 1024 slots cut to
+// 512, 8.0 us, in place 10.6 us.
 #include <cooperative_groups.h>
 
 #include "kv_cache.cuh"

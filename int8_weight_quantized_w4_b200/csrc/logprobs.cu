@@ -15,9 +15,9 @@
 // one of any warp of the CTA (of n unordered logits about top * ln(n / top)
 // pass); to begin with, the top-th largest of the threads' first maxima is such
 // a bound. Lists and sums are joined pairwise by as many warps. Bound by
-// reading the logits (2048 rows of 50257: 69 us, 6.0 TB/s; with 20 alternatives
-// by the insertions, 94 us), by latency where there are few (one row with 5
-// alternatives: 6.9 us; 58 rows with 20: 11.4 us).
+// reading the logits (2048 rows of 50257: 69 us on the device, 6.0 TB/s; with 20
+// alternatives by the insertions, 94 us), by latency where there are few (one row
+// with 5 alternatives: 6.9 us; 58 rows with 20: 11.3 us).
 #include <cooperative_groups.h>
 
 #include "kv_cache.cuh"

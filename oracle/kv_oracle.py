@@ -55,8 +55,8 @@ def kv_attend_ref(q, k, v, scale: float, window: int = 0):
     smallest step, 2^-25, which is 2^-36 of what is stored. So 2^-22 of each
     term is left out, or 2^-36, where the largest q is at least 2^14 and the
     largest weight at least 2^7: 2^-50 of the largest q, 2^-43 of the largest
-    weight, times the largest int8 scale (twice that, a scale lies up to 2
-    above its power of two). A weight is the exponential
+    weight (int8: of the largest weight times scale, so less than the 2^-42 of
+    the largest value that is counted here). A weight is the exponential
     of a difference of two scores (the exponential itself is good to 2^-22),
     and sums of n weights, in any order, rescaled at most once a slot, lose at
     most 2 n roundings."""

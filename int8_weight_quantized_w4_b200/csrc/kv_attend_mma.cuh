@@ -412,7 +412,9 @@ struct MatrixLanes {
       }
       // A tile's products begin at zero and are added here: the matrix pipe cuts
       // its sums off instead of rounding them, which over a warp's thousands of
-      // slots of one sign came to 1.4e-5 of the result.
+      // slots of one sign came to 1.4e-5 of the result. (A score's sum, of 4 to 32
+      // instructions, stays there: 256 products of one sign lose 1.4e-6 of it, all
+      // slots alike, which the log sum shows and the weights do not.)
 #pragma unroll
       for (int cc = 0; cc < NC; ++cc) {
         if constexpr (I8) {
